@@ -23,8 +23,10 @@
  * Around them: dsa_indexer_scores_append (the cache append fused into the indexer's first kernel); two
  * approximate selection variants, block-granular (dsa_block_scores, dsa_expand_blocks) and decode index
  * reuse (dsa_reuse_candidates, dsa_indexer_scores_at, dsa_gather_positions), both ending in dsa_topk;
- * the steps of context-parallel decode across GPUs (dsa_cp_*); and a self-test of the bounded device
- * waits (dsa_selftest_wait_timeout).
+ * the steps of context-parallel decode across GPUs (dsa_cp_*); the serving step's bookkeeping and dense forms:
+ * block tables and slot maps from request lengths (dsa_batch_extend, dsa_batch_release), norms and position
+ * rotation of query and key rows (dsa_qk_norm_rope), one-token attention over every cached page or a list of
+ * pages (dsa_paged_attn_decode); and a self-test of the bounded device waits (dsa_selftest_wait_timeout).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -98,7 +100,11 @@ typedef enum {
   DSA_OP_ATTN_PREFILL = 2,
   DSA_OP_ATTN_DECODE = 3,
   DSA_OP_CACHE_APPEND = 4,
-  DSA_OP_INDEXER_TOPK = 5
+  DSA_OP_INDEXER_TOPK = 5,
+  DSA_OP_PAGED_DECODE = 6,
+  DSA_OP_BATCH_EXTEND = 7,
+  DSA_OP_BATCH_RELEASE = 8,
+  DSA_OP_QK_NORM_ROPE = 9
 } dsa_op_t;
 
 /* Batch descriptor shared by every call.  The three host integers at the end are
@@ -319,6 +325,102 @@ DSA_API dsa_status_t dsa_cp_select_local(const int32_t *sel, const int32_t *g_gi
                                          const int32_t *lo, const int32_t *hi, int32_t *local_idx, void *stream);
 DSA_API dsa_status_t dsa_cp_merge(const void *part_out, dsa_dtype_t dt, const float *part_lse, int32_t G, int32_t T,
                                   int32_t H, int32_t Dv, void *out, float *lse, void *stream);
+
+/* Block tables and slot maps from request lengths ("Day-0 Adaptation: Running Trillion-Parameter Models on
+ * Domestic AI Accelerators", 3.2 KV Cache Layout: paged cache, block table from logical to physical blocks;
+ * "Engineering Practices ...", Four Key Layers 2).  Everything stays on the device: the lengths, the tables and
+ * the stack of free blocks.
+ *
+ * dsa_batch_extend: a step appends new_lens[b] >= 0 tokens to sequence b, which holds cached_lens[b] >= 0.
+ *   block_table[b, ceil(cached/64) ..] = the new pages' blocks, taken from the top of the stack
+ *       (free_blocks[*free_count - 1] first), sequences in order, pages ascending; other entries are untouched
+ *   seq_lens[b] = cached_lens[b] + new_lens[b];  cu_q[b] = sum of new_lens before b
+ *   positions[r] = the position of query row r;  slots[r] = page_size * its block + position % page_size
+ *   *free_left  = free blocks left
+ *   Rows r in [cu_q[num_seqs], total_q) (total_q: capacity of slots and positions) get slot and position -1.
+ *   seq_lens may be cached_lens itself and free_left may be free_count; no other arguments may overlap.
+ *   A step that does not fit (a negative length, a sequence longer than its table row, more rows than total_q,
+ *   fewer free blocks than needed, a count outside [0, free_capacity]) is refused as a whole: the table and the
+ *   stack stay as they were, seq_lens holds the cached lengths (cut to [0, 64 max_blocks_per_seq]), cu_q follows
+ *   the lengths (cut to total_q), every slot and position is -1, and dsa_read_device_status reports
+ *   DSA_ERR_DEVICE_CHECK.  A block id outside [0, num_blocks), on the stack or in an entry that a row needs, is
+ *   reported the same way; rows in that page get slot -1 (and the entry, if new, -1).
+ * dsa_batch_release: sequences with done[b] != 0 give their ceil(seq_lens[b] / 64) blocks back, sequences in
+ *   order, pages ascending, on top of the stack; their seq_lens become 0 and *free_count grows.  Refused as a
+ *   whole (nothing written, DSA_ERR_DEVICE_CHECK) when the stack would pass free_capacity or a length or the
+ *   count is out of range.
+ * cached_lens, new_lens, done, seq_lens [num_seqs] int32; cu_q [num_seqs + 1] int32; block_table [num_seqs,
+ * max_blocks_per_seq] int32; free_blocks [free_capacity] int32; free_count, free_left one int32; slots [total_q]
+ * int64; positions [total_q] int32.  page_size 64.  Workspace: dsa_batch_workspace_size. */
+DSA_API dsa_status_t dsa_batch_workspace_size(dsa_op_t op, int32_t num_seqs, size_t *bytes);
+DSA_API dsa_status_t dsa_batch_extend(const int32_t *cached_lens, const int32_t *new_lens, int32_t num_seqs,
+                                      int32_t page_size, int32_t max_blocks_per_seq, int32_t num_blocks, int32_t total_q,
+                                      const int32_t *free_blocks, int32_t free_capacity, const int32_t *free_count,
+                                      int32_t *block_table, int32_t *seq_lens, int32_t *cu_q, int64_t *slots,
+                                      int32_t *positions, int32_t *free_left, void *ws, size_t ws_bytes, void *stream);
+DSA_API dsa_status_t dsa_batch_release(const int32_t *done, int32_t num_seqs, int32_t page_size,
+                                       int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *block_table,
+                                       int32_t *seq_lens, int32_t *free_blocks, int32_t free_capacity,
+                                       int32_t *free_count, void *ws, size_t ws_bytes, void *stream);
+
+/* RMS norm and position rotation of query and key rows in one pass, one launch for up to four tensors: what turns
+ * the projections of a step into the inputs of the calls above (queries, latent rows, indexer queries and keys;
+ * "Engineering Practices ...", Four Key Layers 3: the decode step writes the new token into the KV cache).
+ * A part is a tensor of rows x[t, h, 0..D), t < T, h < H, at x + t * x_row_stride + h * x_head_stride (elements).
+ * For every row with positions[t] >= 0 (others are left as they were):
+ *   y = x in fp32
+ *   norm_len > 0: over the entries [norm_off, norm_off + norm_len):
+ *       y_i = y_i * weight[i - norm_off] / sqrt(mean of their squares + eps)
+ *   rope_len > 0: over the entries from rope_off, theta_i = positions[t] * inv_freq[i], i < rope_len / 2, entries
+ *       a = 2i, b = 2i + 1 (DSA_ROPE_PAIRS) or a = i, b = i + rope_len / 2 (DSA_ROPE_HALVES):
+ *       (y_a, y_b) = (y_a cos theta_i - y_b sin theta_i, y_b cos theta_i + y_a sin theta_i)
+ *   out row = slots[t] (slots == NULL: t; a negative slot: the row is skipped), at out + row * out_row_stride +
+ *       h * out_head_stride: y rounded once to out_dt (e4m3 saturates at +-448)
+ *   out_scale != NULL (e4m3 only): out_scale[row * H + h] = max|y| / 448 (1 if that is 0), codes of y / scale --
+ *       the form dsa_cache_append stores indexer keys in.
+ * Angles are reduced in 64 bits, so far positions lose nothing.  out may be x itself (same strides, no slots).  A
+ * slot >= out_rows is skipped and reported as DSA_ERR_DEVICE_CHECK; two rows with the same slot race.
+ *   x_dt f32 or bf16;  out_dt f32, bf16 or e4m3;  weight [norm_len] of w_dt f32 or bf16;  positions [T] int32
+ *   (NULL only when no part rotates: every row is taken);  inv_freq [rope_len / 2] f64 radians per position, shared
+ *   by the parts, whose non-zero rope_len must be equal;  slots [T] int64.
+ * Supported: 1 to 4 parts; D a multiple of 8 in [8, 1024]; norm_off, norm_len and rope_off multiples of 8; rope_len a
+ * multiple of 16 up to 256; out strides >= D.  The workspace only carries the status word (256 bytes). */
+typedef enum { DSA_ROPE_PAIRS = 0, DSA_ROPE_HALVES = 1 } dsa_rope_style_t;
+typedef struct {
+  const void *x;
+  void *out;
+  const void *weight;          /* NULL when norm_len == 0 */
+  float *out_scale;            /* NULL: no scale */
+  const int64_t *slots;        /* NULL: out row t */
+  int64_t x_row_stride, x_head_stride, out_row_stride, out_head_stride;   /* elements */
+  int64_t out_rows;            /* rows that out holds */
+  int32_t H, D;
+  int32_t norm_off, norm_len, rope_off, rope_len;
+  dsa_dtype_t x_dt, w_dt, out_dt;
+  dsa_rope_style_t rope_style;
+  float eps;
+} dsa_rope_part_t;
+DSA_API dsa_status_t dsa_qk_norm_rope(const dsa_rope_part_t *parts, int32_t num_parts, const int32_t *positions, int32_t T,
+                                      const double *inv_freq, void *ws, size_t ws_bytes, void *stream);
+
+/* Attention of one new token per sequence over the paged cache, split over the cache's length and joined
+ * ("Engineering Practices ...", Four Key Layers 3: partial results merged by a cross-block reduction).  Row b is
+ * the last token of sequence b (total_q == num_seqs, cu_q[b] = b) and attends to
+ *   pages == NULL (kb = 0): all its seq_lens[b] cached tokens;
+ *   pages [num_seqs, kb] int32: the tokens below seq_lens[b] of the logical pages in its list, in any order; -1 and
+ *     pages past the sequence are skipped, a page named twice counts twice.  This is block-granular sparse attention
+ *     on the pages that dsa_topk keeps of dsa_block_scores ("Day-0 Adaptation: Running Trillion-Parameter Models on
+ *     Domestic AI Accelerators", 3.1), without expanding them to token positions.
+ * Arguments, out and lse as in dsa_sparse_attn_decode; a row without tokens (seq_lens[b] = 0, or nothing in its list)
+ * gives zeros and -inf.  What the cache holds past a sequence's last token never reaches a result.
+ * Supported: bf16 latent cache with Dqk = 576, Dv = 512, v_pool NULL and 1 <= H <= 128 (a head shard of any size);
+ * f32 with H <= 16, Dqk <= 128, Dv <= 128 and a separate v_pool; num_seqs * page slots < 2^31; num_blocks < 2^25.
+ * Results do not depend on timing.  A block id outside [0, num_blocks) leaves its page out and a sequence longer than
+ * its table row is cut; dsa_read_device_status reports both.  Workspace: dsa_workspace_size(DSA_OP_PAGED_DECODE). */
+DSA_API dsa_status_t dsa_paged_attn_decode(const void *q, dsa_dtype_t dt, const void *kv_pool, const void *v_pool,
+                                           int32_t H, int32_t Dqk, int32_t Dv, float softmax_scale, const int32_t *pages,
+                                           int32_t kb, const dsa_batch_t *b, void *out, float *lse, void *ws,
+                                           size_t ws_bytes, void *stream);
 
 /* Self-test of the bounded device waits: enqueues one kernel whose thread waits on an mbarrier that
  * nothing completes, through the wait routine every tensor-core kernel uses, with a budget of

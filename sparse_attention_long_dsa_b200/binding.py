@@ -19,13 +19,16 @@ DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE, DSA_ERR_CUD
 DSA_F32, DSA_BF16, DSA_FP8_E4M3 = 0, 1, 2
 DSA_OP_INDEXER, DSA_OP_TOPK, DSA_OP_ATTN_PREFILL, DSA_OP_ATTN_DECODE, DSA_OP_CACHE_APPEND, DSA_OP_INDEXER_TOPK = \
     0, 1, 2, 3, 4, 5
+DSA_OP_PAGED_DECODE, DSA_OP_BATCH_EXTEND, DSA_OP_BATCH_RELEASE, DSA_OP_QK_NORM_ROPE = 6, 7, 8, 9
+DSA_ROPE_PAIRS, DSA_ROPE_HALVES = 0, 1
 
 EXPORTS = ("dsa_workspace_size", "dsa_indexer_scores", "dsa_topk", "dsa_sparse_attn_prefill",
            "dsa_sparse_attn_decode", "dsa_read_device_status", "dsa_status_string", "dsa_last_error",
            "dsa_version", "dsa_launch_count", "dsa_topk_noalloc", "dsa_cache_append", "dsa_selftest_wait_timeout",
            "dsa_cp_candidates", "dsa_cp_rows", "dsa_cp_select_local", "dsa_cp_merge", "dsa_block_scores",
            "dsa_expand_blocks", "dsa_reuse_candidates", "dsa_indexer_scores_at", "dsa_gather_positions",
-           "dsa_indexer_scores_append", "dsa_indexer_topk")
+           "dsa_indexer_scores_append", "dsa_indexer_topk", "dsa_batch_workspace_size", "dsa_batch_extend",
+           "dsa_batch_release", "dsa_qk_norm_rope", "dsa_paged_attn_decode")
 
 
 class dsa_batch_t(ctypes.Structure):
@@ -40,6 +43,32 @@ class dsa_batch_t(ctypes.Structure):
         ("total_q", ctypes.c_int32),
         ("max_q_per_seq", ctypes.c_int32),
         ("max_seq_len", ctypes.c_int32),
+    ]
+
+
+class dsa_rope_part_t(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("out_scale", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+        ("x_row_stride", ctypes.c_int64),
+        ("x_head_stride", ctypes.c_int64),
+        ("out_row_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+        ("out_rows", ctypes.c_int64),
+        ("H", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("norm_off", ctypes.c_int32),
+        ("norm_len", ctypes.c_int32),
+        ("rope_off", ctypes.c_int32),
+        ("rope_len", ctypes.c_int32),
+        ("x_dt", ctypes.c_int),
+        ("w_dt", ctypes.c_int),
+        ("out_dt", ctypes.c_int),
+        ("rope_style", ctypes.c_int),
+        ("eps", ctypes.c_float),
     ]
 
 
@@ -83,6 +112,11 @@ def load(path: str = LIB_PATH):
         "dsa_cp_rows": [P, I32, I32, I32, P, I64, P],
         "dsa_cp_select_local": [P, P, I32, I32, I32, P, P, P, P],
         "dsa_cp_merge": [P, I32, P, I32, I32, I32, I32, P, P, P],
+        "dsa_batch_workspace_size": [I32, I32, ctypes.POINTER(SZ)],
+        "dsa_batch_extend": [P, P, I32, I32, I32, I32, I32, P, I32, P, P, P, P, P, P, P, P, SZ, P],
+        "dsa_batch_release": [P, I32, I32, I32, I32, P, P, P, I32, P, P, SZ, P],
+        "dsa_qk_norm_rope": [ctypes.POINTER(dsa_rope_part_t), I32, P, I32, P, P, SZ, P],
+        "dsa_paged_attn_decode": [P, I32, P, P, I32, I32, I32, F, P, I32, B, P, P, P, SZ, P],
         "dsa_read_device_status": [P, P],
     }
     for name, args in sig.items():
@@ -254,6 +288,149 @@ def dsa_cp_select_local(sel, g_gidx, G: int, T: int, k: int, lo, hi, local_idx, 
 def dsa_cp_merge(part_out, dt: int, part_lse, G: int, T: int, H: int, Dv: int, out, lse, stream=None):
     _check(load().dsa_cp_merge(_ptr(part_out), dt, _ptr(part_lse), G, T, H, Dv, _ptr(out), _ptr(lse),
                                _stream(stream)), "dsa_cp_merge")
+
+
+def _arg(t, dtypes: tuple, what: str):
+    """A dense tensor of one of the named dtypes on the current device: its address."""
+    import torch
+    if str(t.dtype)[6:] not in dtypes:
+        raise DSAError(DSA_ERR_INVALID_ARG, what, f"dtype {t.dtype}; expected {' or '.join(dtypes)}")
+    p = _ptr(t)
+    if t.device.index != torch.cuda.current_device():
+        raise DSAError(DSA_ERR_INVALID_ARG, what, f"a tensor on {t.device}; the current device is "
+                                                  f"cuda:{torch.cuda.current_device()}")
+    return p
+
+
+_INT = ("int32",)
+
+
+def _shape(t, shape: tuple, what: str):
+    if tuple(t.shape) != shape:
+        raise DSAError(DSA_ERR_INVALID_ARG, what, f"shape {tuple(t.shape)}; expected {shape}")
+
+
+def dsa_batch_workspace_size(op: int, num_seqs: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().dsa_batch_workspace_size(op, num_seqs, ctypes.byref(out)), "dsa_batch_workspace_size")
+    return out.value
+
+
+def dsa_batch_extend(cached_lens, new_lens, page_size: int, num_blocks: int, total_q: int, free_blocks, free_count,
+                     block_table, seq_lens, cu_q, slots, positions, free_left, ws, ws_bytes: int, stream=None):
+    """Block tables, slots and positions of a step, from device lengths (cached_lens, new_lens [B]): block_table [B,
+    max_blocks] and the stack free_blocks / free_count lose and gain pages on the device.  seq_lens may be cached_lens
+    and free_left may be free_count."""
+    w = "dsa_batch_extend"
+    n = cached_lens.numel()
+    _shape(new_lens, (n,), w)
+    _shape(seq_lens, (n,), w)
+    _shape(cu_q, (n + 1,), w)
+    if block_table.dim() != 2 or block_table.shape[0] != n or slots.numel() < total_q or positions.numel() < total_q:
+        raise DSAError(DSA_ERR_INVALID_ARG, w, f"block_table [{n}, max_blocks], slots and positions [total_q] expected")
+    _check(load().dsa_batch_extend(
+        _arg(cached_lens, _INT, w), _arg(new_lens, _INT, w), n, page_size, block_table.shape[1], num_blocks, total_q,
+        _arg(free_blocks, _INT, w), free_blocks.numel(), _arg(free_count, _INT, w), _arg(block_table, _INT, w),
+        _arg(seq_lens, _INT, w), _arg(cu_q, _INT, w), _arg(slots, ("int64",), w), _arg(positions, _INT, w),
+        _arg(free_left, _INT, w), _ptr(ws), ws_bytes, _stream(stream)), w)
+
+
+def dsa_batch_release(done, page_size: int, num_blocks: int, block_table, seq_lens, free_blocks, free_count, ws,
+                      ws_bytes: int, stream=None):
+    """Gives the blocks of the sequences with done[b] != 0 back to the stack; their seq_lens become 0."""
+    w = "dsa_batch_release"
+    n = done.numel()
+    _shape(seq_lens, (n,), w)
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise DSAError(DSA_ERR_INVALID_ARG, w, f"block_table [{n}, max_blocks] expected")
+    _check(load().dsa_batch_release(
+        _arg(done, _INT, w), n, page_size, block_table.shape[1], num_blocks, _arg(block_table, _INT, w),
+        _arg(seq_lens, _INT, w), _arg(free_blocks, _INT, w), free_blocks.numel(), _arg(free_count, _INT, w), _ptr(ws),
+        ws_bytes, _stream(stream)), w)
+
+
+def rope_part(x, out, *, weight=None, norm=(0, 0), eps: float = 1e-6, rope=(0, 0), style: str = "pairs", slots=None,
+              scale=None) -> dsa_rope_part_t:
+    """One tensor of dsa_qk_norm_rope: x [T, H, D] or [T, D] (f32 or bf16, any strides with a dense last dimension; so a
+    view of a fused projection), out [N, H, D] or [N, D] (f32, bf16, e4m3 or uint8 for e4m3 codes; a view too).  norm and
+    rope are (offset, length) in entries of a row, style "pairs" or "halves", slots [T] int64 out rows, scale [N, H] or
+    [N] f32.  The part holds the tensors' addresses and keeps the tensors alive."""
+    w = "rope_part"
+    floats, codes = {"float32": DSA_F32, "bfloat16": DSA_BF16}, {"uint8": DSA_FP8_E4M3, "float8_e4m3fn": DSA_FP8_E4M3}
+
+    def fail(msg):
+        raise DSAError(DSA_ERR_INVALID_ARG, w, msg)
+
+    def view(t, name, kinds):
+        if not t.is_cuda:
+            fail(f"{name} on {t.device}; the library takes device memory")
+        if t.device != x.device:
+            fail(f"{name} on {t.device}, x on {x.device}")
+        kind = kinds.get(str(t.dtype)[6:])
+        if kind is None:
+            fail(f"{name} is {t.dtype}; expected {' or '.join(kinds)}")
+        if t.dim() not in (2, 3) or (t.shape[-1] > 1 and t.stride(-1) != 1):
+            fail(f"{name} must be [rows, heads, D] or [rows, D] with a dense last dimension")
+        if t.dim() == 2:
+            return kind, t.shape[0], 1, t.shape[1], t.stride(0), t.shape[1]
+        return kind, t.shape[0], t.shape[1], t.shape[2], t.stride(0), t.stride(1)
+
+    x_dt, T, H, D, x_row, x_head = view(x, "x", floats)
+    o_dt, rows, o_h, o_d, o_row, o_head = view(out, "out", {**floats, **codes})
+    if (o_h, o_d) != (H, D):
+        fail(f"out rows are [{o_h}, {o_d}], x rows [{H}, {D}]")
+    if rows == 1:
+        o_row = max(o_row, D)
+    if style not in ("pairs", "halves"):
+        fail(f"style {style!r}; expected 'pairs' or 'halves'")
+    if slots is not None and (str(slots.dtype) != "torch.int64" or tuple(slots.shape) != (T,)):
+        fail("slots must be [T] int64")
+    if scale is not None and (str(scale.dtype) != "torch.float32" or scale.numel() != rows * H):
+        fail("scale must be [rows, H] float32")
+    if norm[1] and (weight is None or weight.numel() != norm[1] or str(weight.dtype)[6:] not in floats):
+        fail("a norm needs a weight of its length, f32 or bf16")
+    part = dsa_rope_part_t(x=x.data_ptr(), out=out.data_ptr(), weight=_ptr(weight), out_scale=_ptr(scale),
+                           slots=_ptr(slots), x_row_stride=x_row, x_head_stride=x_head, out_row_stride=o_row,
+                           out_head_stride=o_head, out_rows=rows, H=H, D=D, norm_off=norm[0], norm_len=norm[1],
+                           rope_off=rope[0], rope_len=rope[1], x_dt=x_dt,
+                           w_dt=floats[str(weight.dtype)[6:]] if weight is not None else DSA_F32, out_dt=o_dt,
+                           rope_style=DSA_ROPE_HALVES if style == "halves" else DSA_ROPE_PAIRS, eps=eps)
+    part.rows = T
+    part.device = x.device
+    part.tensors = (x, out, weight, scale, slots)
+    return part
+
+
+def dsa_qk_norm_rope(parts, positions, inv_freq, ws, ws_bytes: int, stream=None):
+    """RMS norm and position rotation of up to four tensors (rope_part) in one launch: positions [T] int32, inv_freq
+    [rope_len / 2] float64."""
+    w = "dsa_qk_norm_rope"
+    if not 1 <= len(parts) <= 4:
+        raise DSAError(DSA_ERR_UNSUPPORTED, w, f"{len(parts)} parts; 1 to 4 are taken")
+    T = parts[0].rows
+    import torch
+    for p in parts:
+        if p.rows != T:
+            raise DSAError(DSA_ERR_INVALID_ARG, w, f"parts of {T} and {p.rows} rows")
+        if p.device.index != torch.cuda.current_device():
+            raise DSAError(DSA_ERR_INVALID_ARG, w, f"a part on {p.device}; the current device is "
+                                                   f"cuda:{torch.cuda.current_device()}")
+        if inv_freq is not None and p.rope_len and inv_freq.numel() != p.rope_len // 2:
+            raise DSAError(DSA_ERR_INVALID_ARG, w, f"{inv_freq.numel()} frequencies for rope_len {p.rope_len}")
+    if positions is not None:
+        _shape(positions, (T,), w)
+    arr = (dsa_rope_part_t * len(parts))(*parts)
+    _check(load().dsa_qk_norm_rope(arr, len(parts), None if positions is None else _arg(positions, _INT, w), T,
+                                   None if inv_freq is None else _arg(inv_freq, ("float64",), w), _ptr(ws), ws_bytes,
+                                   _stream(stream)), w)
+
+
+def dsa_paged_attn_decode(q, dt: int, kv_pool, v_pool, H: int, Dqk: int, Dv: int, softmax_scale: float, pages, kb: int,
+                          batch: dsa_batch_t, out, lse, ws, ws_bytes: int, stream=None):
+    """Attention of one new token per sequence over every cached page, or over its list of pages [B, kb]."""
+    _check(load().dsa_paged_attn_decode(_ptr(q), dt, _ptr(kv_pool), _ptr(v_pool), H, Dqk, Dv, softmax_scale, _ptr(pages),
+                                        kb, ctypes.byref(batch), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
+                                        _stream(stream)), "dsa_paged_attn_decode")
 
 
 def dsa_read_device_status(ws, stream=None):

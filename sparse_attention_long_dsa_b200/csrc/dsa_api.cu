@@ -54,6 +54,20 @@ dsa_status_t cp_select_local_launch(const int32_t *sel, const int32_t *g_gidx, i
                                     const int32_t *hi, int32_t *local, cudaStream_t stream);
 dsa_status_t cp_merge_launch(const void *part_out, const float *part_lse, int G, int T, int H, int Dv, void *out,
                              float *lse, cudaStream_t stream);
+size_t batch_tables_ws_bytes(int num_seqs);
+dsa_status_t batch_extend_launch(const int32_t *cached, const int32_t *add, int num_seqs, int max_blocks, int num_blocks,
+                                 int total_q, const int32_t *free_blocks, int free_cap, const int32_t *free_count,
+                                 int32_t *table, int32_t *seq_lens, int32_t *cu_q, int64_t *slots, int32_t *positions,
+                                 int32_t *free_left, void *ws, cudaStream_t stream);
+dsa_status_t batch_release_launch(const int32_t *done, int num_seqs, int max_blocks, int num_blocks, const int32_t *table,
+                                  int32_t *seq_lens, int32_t *free_blocks, int free_cap, int32_t *free_count, void *ws,
+                                  cudaStream_t stream);
+dsa_status_t qk_rope_launch(const dsa_rope_part_t *parts, int nparts, const int32_t *positions, int T,
+                            const double *inv_freq, void *ws, cudaStream_t stream);
+size_t paged_workspace_bytes(int H, int Dv);
+dsa_status_t paged_attn_launch(const void *q, bool bf16, const void *kv, const void *v, int H, int Dqk, int Dv,
+                               float scale, const int32_t *pages, int kb, const dsa_batch_t *b, void *out, float *lse,
+                               void *ws, cudaStream_t stream, int num_sms);
 dsa_status_t attn_simt_launch(const void *q, dsa_dtype_t dt, const void *kv, const void *v, int H, int Dqk, int Dv,
                               float scale, const int32_t *idx, int k, const dsa_batch_t *b, void *out, float *lse,
                               cudaStream_t stream);
@@ -202,6 +216,13 @@ dsa_status_t dsa_workspace_size(dsa_op_t op, const dsa_batch_t *b, int32_t k, in
     case DSA_OP_ATTN_DECODE: *bytes = attn_ws_bytes(b, k, H, Dv, true); return DSA_OK;
     case DSA_OP_CACHE_APPEND: *bytes = kWsHeader; return DSA_OK;
     case DSA_OP_INDEXER_TOPK: *bytes = indexer_topk_ws_bytes(b); return DSA_OK;
+    case DSA_OP_PAGED_DECODE:
+      CHECK_ARG(H >= 1 && H <= 128 && Dv >= 1 && Dv <= 512, "paged decode: H must be in [1, 128] and Dv in [1, 512]");
+      *bytes = paged_workspace_bytes(H, Dv);
+      return DSA_OK;
+    case DSA_OP_BATCH_EXTEND:
+    case DSA_OP_BATCH_RELEASE: *bytes = batch_tables_ws_bytes(b->num_seqs); return DSA_OK;
+    case DSA_OP_QK_NORM_ROPE: *bytes = kWsHeader; return DSA_OK;
   }
   set_error("unknown op %d", (int)op);
   return DSA_ERR_INVALID_ARG;
@@ -528,6 +549,147 @@ dsa_status_t dsa_cp_merge(const void *part_out, dsa_dtype_t dt, const float *par
   dsa_status_t st;
   if ((st = current_device(&dev)) != DSA_OK) return st;
   return cp_merge_launch(part_out, part_lse, G, T, H, Dv, out, lse, (cudaStream_t)stream);
+}
+
+dsa_status_t dsa_batch_workspace_size(dsa_op_t op, int32_t num_seqs, size_t *bytes) {
+  CHECK_ARG(bytes != nullptr, "bytes is NULL");
+  CHECK_ARG(op == DSA_OP_BATCH_EXTEND || op == DSA_OP_BATCH_RELEASE, "op %d takes dsa_workspace_size", (int)op);
+  CHECK_ARG(num_seqs >= 1, "num_seqs must be >= 1 (got %d)", num_seqs);
+  *bytes = batch_tables_ws_bytes(num_seqs);
+  return DSA_OK;
+}
+
+static dsa_status_t check_tables(int32_t num_seqs, int32_t page_size, int32_t max_blocks, int32_t num_blocks,
+                                 int32_t free_cap) {
+  CHECK_ARG(num_seqs >= 1, "num_seqs must be >= 1 (got %d)", num_seqs);
+  CHECK_SUP(page_size == 64, "page_size must be 64 (got %d)", page_size);
+  CHECK_ARG(num_blocks >= 1 && max_blocks >= 1, "num_blocks and max_blocks_per_seq must be >= 1");
+  CHECK_SUP(max_blocks <= 0x7FFFFFFF / 64, "max_blocks_per_seq * page_size must fit in int32");
+  CHECK_ARG(free_cap >= 0, "free_capacity must be >= 0");
+  return DSA_OK;
+}
+
+dsa_status_t dsa_batch_extend(const int32_t *cached_lens, const int32_t *new_lens, int32_t num_seqs, int32_t page_size,
+                              int32_t max_blocks_per_seq, int32_t num_blocks, int32_t total_q, const int32_t *free_blocks,
+                              int32_t free_capacity, const int32_t *free_count, int32_t *block_table, int32_t *seq_lens,
+                              int32_t *cu_q, int64_t *slots, int32_t *positions, int32_t *free_left, void *ws,
+                              size_t ws_bytes, void *stream) {
+  dsa_status_t st = check_tables(num_seqs, page_size, max_blocks_per_seq, num_blocks, free_capacity);
+  if (st != DSA_OK) return st;
+  CHECK_ARG(total_q >= 0, "total_q must be >= 0");
+  CHECK_ARG(cached_lens && new_lens && free_count && free_left && block_table && seq_lens && cu_q,
+            "cached_lens, new_lens, free_count, free_left, block_table, seq_lens and cu_q are required");
+  CHECK_ARG(free_capacity == 0 || free_blocks, "free_blocks is required");
+  CHECK_ARG(total_q == 0 || (slots && positions), "slots and positions are required");
+  CHECK_ARG(new_lens != seq_lens && new_lens != cached_lens, "new_lens may not be cached_lens or seq_lens");
+  if ((st = check_ws(ws, ws_bytes, batch_tables_ws_bytes(num_seqs))) != DSA_OK) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != DSA_OK) return st;
+  return batch_extend_launch(cached_lens, new_lens, num_seqs, max_blocks_per_seq, num_blocks, total_q, free_blocks,
+                             free_capacity, free_count, block_table, seq_lens, cu_q, slots, positions, free_left, ws,
+                             (cudaStream_t)stream);
+}
+
+dsa_status_t dsa_batch_release(const int32_t *done, int32_t num_seqs, int32_t page_size, int32_t max_blocks_per_seq,
+                               int32_t num_blocks, const int32_t *block_table, int32_t *seq_lens, int32_t *free_blocks,
+                               int32_t free_capacity, int32_t *free_count, void *ws, size_t ws_bytes, void *stream) {
+  dsa_status_t st = check_tables(num_seqs, page_size, max_blocks_per_seq, num_blocks, free_capacity);
+  if (st != DSA_OK) return st;
+  CHECK_ARG(done && block_table && seq_lens && free_count, "done, block_table, seq_lens and free_count are required");
+  CHECK_ARG(done != seq_lens, "done may not be seq_lens");
+  CHECK_ARG(free_capacity == 0 || free_blocks, "free_blocks is required");
+  if ((st = check_ws(ws, ws_bytes, batch_tables_ws_bytes(num_seqs))) != DSA_OK) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != DSA_OK) return st;
+  return batch_release_launch(done, num_seqs, max_blocks_per_seq, num_blocks, block_table, seq_lens, free_blocks,
+                              free_capacity, free_count, ws, (cudaStream_t)stream);
+}
+
+static dsa_status_t check_rope_part(const dsa_rope_part_t *p, int i, int32_t T, const int32_t *positions,
+                                    const double *inv_freq, int32_t *rope_len) {
+  CHECK_ARG(p->x && p->out, "part %d: x and out are required", i);
+  CHECK_ARG(p->H >= 1, "part %d: H must be >= 1 (got %d)", i, p->H);
+  CHECK_SUP(p->D >= 8 && p->D <= 1024 && p->D % 8 == 0, "part %d: D must be a multiple of 8 in [8, 1024] (got %d)", i, p->D);
+  CHECK_SUP(p->x_dt == DSA_F32 || p->x_dt == DSA_BF16, "part %d: x must be f32 or bf16", i);
+  CHECK_SUP(p->out_dt == DSA_F32 || p->out_dt == DSA_BF16 || p->out_dt == DSA_FP8_E4M3,
+            "part %d: out must be f32, bf16 or e4m3", i);
+  CHECK_ARG(p->norm_off >= 0 && p->norm_len >= 0 && (int64_t)p->norm_off + p->norm_len <= p->D,
+            "part %d: the normed entries lie outside the row", i);
+  CHECK_ARG(p->rope_off >= 0 && p->rope_len >= 0 && (int64_t)p->rope_off + p->rope_len <= p->D,
+            "part %d: the rotated entries lie outside the row", i);
+  if (p->norm_len > 0) {
+    CHECK_SUP(p->norm_off % 8 == 0 && p->norm_len % 8 == 0, "part %d: norm_off and norm_len must be multiples of 8", i);
+    CHECK_ARG(p->weight != nullptr, "part %d: weight is required", i);
+    CHECK_SUP(p->w_dt == DSA_F32 || p->w_dt == DSA_BF16, "part %d: weight must be f32 or bf16", i);
+    CHECK_ARG(p->eps >= 0.f && p->eps < 1e30f, "part %d: eps must be finite and not negative", i);
+  }
+  if (p->rope_len > 0) {
+    CHECK_SUP(p->rope_off % 8 == 0 && p->rope_len % 16 == 0 && p->rope_len <= 256,
+              "part %d: rope_off must be a multiple of 8, rope_len a multiple of 16 up to 256", i);
+    CHECK_ARG(p->rope_style == DSA_ROPE_PAIRS || p->rope_style == DSA_ROPE_HALVES, "part %d: unknown rope_style %d", i,
+              (int)p->rope_style);
+    CHECK_ARG(positions && inv_freq, "positions and inv_freq are required to rotate");
+    CHECK_ARG(*rope_len == 0 || *rope_len == p->rope_len, "part %d: rope_len %d differs from another part's %d", i,
+              p->rope_len, *rope_len);
+    *rope_len = p->rope_len;
+  }
+  CHECK_ARG(p->out_scale == nullptr || p->out_dt == DSA_FP8_E4M3, "part %d: out_scale goes with e4m3 output", i);
+  CHECK_ARG(p->x_row_stride >= 0 && p->x_head_stride >= 0, "part %d: negative strides", i);
+  CHECK_ARG(p->out_row_stride >= p->D && (p->H == 1 || p->out_head_stride >= p->D),
+            "part %d: output rows and heads overlap", i);
+  CHECK_ARG(p->slots ? p->out_rows >= 1 : p->out_rows >= T, "part %d: out_rows (%lld) is too small", i,
+            (long long)p->out_rows);
+  const uintptr_t xa = p->x_dt == DSA_F32 ? 3 : 1;
+  const uintptr_t oa = p->out_dt == DSA_F32 ? 3 : p->out_dt == DSA_BF16 ? 1 : 0;
+  const uintptr_t wa = p->norm_len == 0 ? 0 : p->w_dt == DSA_F32 ? 3 : 1;
+  CHECK_ARG(((uintptr_t)p->x & xa) == 0 && ((uintptr_t)p->out & oa) == 0 && ((uintptr_t)p->weight & wa) == 0 &&
+                ((uintptr_t)p->out_scale & 3) == 0 && ((uintptr_t)p->slots & 7) == 0,
+            "part %d: a buffer is not aligned to its element size", i);
+  return DSA_OK;
+}
+
+dsa_status_t dsa_qk_norm_rope(const dsa_rope_part_t *parts, int32_t num_parts, const int32_t *positions, int32_t T,
+                              const double *inv_freq, void *ws, size_t ws_bytes, void *stream) {
+  CHECK_ARG(T >= 0, "T must be >= 0");
+  CHECK_ARG(parts != nullptr, "parts is required");
+  CHECK_SUP(num_parts >= 1 && num_parts <= 4, "num_parts must be in [1, 4] (got %d)", num_parts);
+  if (T == 0) return DSA_OK;   // empty batch: nothing to enqueue, data pointers may be NULL
+  dsa_status_t st;
+  int32_t rope_len = 0;
+  for (int32_t i = 0; i < num_parts; ++i)
+    if ((st = check_rope_part(parts + i, i, T, positions, inv_freq, &rope_len)) != DSA_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, kWsHeader)) != DSA_OK) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != DSA_OK) return st;
+  return qk_rope_launch(parts, num_parts, positions, T, inv_freq, ws, (cudaStream_t)stream);
+}
+
+dsa_status_t dsa_paged_attn_decode(const void *q, dsa_dtype_t dt, const void *kv_pool, const void *v_pool, int32_t H,
+                                   int32_t Dqk, int32_t Dv, float softmax_scale, const int32_t *pages, int32_t kb,
+                                   const dsa_batch_t *b, void *out, float *lse, void *ws, size_t ws_bytes, void *stream) {
+  dsa_status_t st = check_batch(b);
+  if (st != DSA_OK) return st;
+  if (b->total_q == 0) return DSA_OK;   // empty batch: nothing to enqueue, data pointers may be NULL
+  CHECK_ARG(q && kv_pool && out, "q, kv_pool and out are required");
+  CHECK_ARG(pages ? kb >= 1 : kb == 0, "kb must be >= 1 with a page list and 0 without (got %d)", kb);
+  CHECK_ARG(softmax_scale == softmax_scale && softmax_scale > 0.f && softmax_scale < 1e30f,
+            "softmax_scale must be finite and positive");
+  const bool mla = dt == DSA_BF16 && H >= 1 && H <= 128 && Dqk == 576 && Dv == 512 && v_pool == nullptr;
+  const bool f32 = is_f32_attn(dt, H, Dqk, Dv, v_pool);
+  CHECK_SUP(mla || f32,
+            "paged decode supports a bf16 latent cache (H <= 128, Dqk=576, Dv=512, V inside the latent row) or f32 with "
+            "H<=16, Dqk<=128, Dv<=128 and a separate V cache");
+  CHECK_ARG(b->total_q == b->num_seqs && b->max_q_per_seq == 1, "decode needs exactly one query row per sequence");
+  const int64_t width = pages ? kb : b->max_blocks_per_seq;
+  CHECK_SUP((int64_t)b->num_seqs * width <= 0x7FFFFFFF, "num_seqs * page slots must fit in int32");
+  CHECK_SUP(b->num_blocks < 1 << 25, "num_blocks must be below 2^25");
+  CHECK_ARG((((uintptr_t)q | (uintptr_t)kv_pool | (uintptr_t)v_pool | (uintptr_t)out) & 15) == 0,
+            "q, kv_pool, v_pool and out must be 16-byte aligned");
+  if ((st = check_ws(ws, ws_bytes, paged_workspace_bytes(H, Dv))) != DSA_OK) return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != DSA_OK) return st;
+  return paged_attn_launch(q, mla, kv_pool, v_pool, H, Dqk, Dv, softmax_scale, pages, kb, b, out, lse, ws,
+                           (cudaStream_t)stream, dev.num_sms);
 }
 
 dsa_status_t dsa_read_device_status(void *ws, void *stream) {

@@ -1,0 +1,156 @@
+// One-token attention over the paged cache: how its kernels walk the pages of a batch.
+//
+// Every row of a decode batch has a number of page slots (all pages of its sequence, or the kb entries of its page
+// list).  The slots of all rows, one row after another, form one flat range of P slots, and worker w of np takes
+// the slots [floor(w P / np), floor((w + 1) P / np)): contiguous, equal to within one page whatever the lengths
+// are, and known to every worker from the lengths alone (they stay on the device).  The piece of a row inside a
+// worker's range is a segment.  A segment that holds its whole row writes the row's result; the others write a
+// partial result, normalised with its log-sum-exp, to a slot of the workspace: slot 2w + 1 when the row starts in
+// worker w (and goes on), 2w when it started before.  Worker w notes in info[w] the row that ends in it after
+// starting elsewhere, and the combine kernel joins that row's partials in the workers' order, so results do not
+// depend on timing.
+#pragma once
+
+#include "common.cuh"
+
+namespace dsa {
+
+constexpr int kPage = 64;
+
+struct PagedView {
+  const int32_t *block_table;   // [T, max_blocks]
+  const int32_t *seq_lens;      // [T]
+  const int32_t *pages;         // [T, kb] or nullptr: every page
+  int T, kb, max_blocks, num_blocks;
+};
+
+struct PagedOut {
+  void *out;                    // [T, H, Dv]
+  float *lse;                   // [T, H] or nullptr
+  float *part_o;                // [2 workers, H, Dv]
+  float *part_lse;              // [2 workers, H]
+  int2 *info;                   // [workers] (row, first worker), row -1: none
+  uint32_t *status;
+};
+
+struct PagedPlan {
+  uint32_t total;               // P
+  uint32_t start, end;          // this worker's slots
+  int np;                       // workers that have any
+  int row, page;                // where `start` lies
+};
+
+__device__ __forceinline__ int row_slots(const PagedView &v, int row) {
+  const int n = __ldg(v.seq_lens + row);
+  if (n <= 0) return 0;
+  if (v.pages) return v.kb;
+  const int p = (int)(((int64_t)n + kPage - 1) / kPage);
+  return p < v.max_blocks ? p : v.max_blocks;
+}
+
+// cached tokens of a row, cut to what its block-table row can hold
+__device__ __forceinline__ int row_tokens(const PagedView &v, int row, uint32_t *status) {
+  const int n = __ldg(v.seq_lens + row);
+  const int64_t cap = (int64_t)v.max_blocks * kPage;
+  if (n > cap) {
+    set_status(status, kStatusBadIndex);
+    return (int)cap;
+  }
+  return n;
+}
+
+// tokens that slot i of a row holds, and its physical block; 0 tokens: the slot is skipped
+__device__ __forceinline__ int slot_tokens(const PagedView &v, int row, int n, int i, int *block, uint32_t *status) {
+  int pg = i;
+  if (v.pages) pg = __ldg(v.pages + (int64_t)row * v.kb + i);
+  if (pg < 0 || pg >= v.max_blocks || pg * (int64_t)kPage >= n) return 0;
+  const int blk = __ldg(v.block_table + (int64_t)row * v.max_blocks + pg);
+  if ((unsigned)blk >= (unsigned)v.num_blocks) {
+    set_status(status, kStatusBadIndex);
+    return 0;
+  }
+  *block = blk;
+  const int left = n - pg * kPage;
+  return left < kPage ? left : kPage;
+}
+
+__device__ __forceinline__ int worker_of_slot(uint32_t f, const PagedPlan &p) {
+  return (int)((((uint64_t)f + 1) * (uint64_t)p.np - 1) / p.total);
+}
+
+// Every thread of the block calls this (blockDim.x a multiple of 32, at most 1024); `tmp` holds 33 words.
+__device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int workers, int min_slots, uint32_t *tmp,
+                                           PagedPlan *p) {
+  const int nt = blockDim.x, per = (v.T + nt - 1) / nt;
+  const int r0 = min(v.T, (int)threadIdx.x * per), r1 = min(v.T, r0 + per);
+  uint32_t mine = 0;
+  for (int r = r0; r < r1; ++r) mine += (uint32_t)row_slots(v, r);
+  uint32_t total;
+  const uint32_t before = block_exclusive_scan(mine, tmp, &total);
+  // a worker for every min_slots page slots: fewer workers than that pay more for their partials than they save
+  const uint32_t want = total / (uint32_t)min_slots;
+  const int np = want < 1u ? 1 : (want < (uint32_t)workers ? (int)want : workers);
+  const bool any = worker < np;
+  const uint32_t start = any ? (uint32_t)((uint64_t)worker * total / np) : total;
+  const uint32_t end = any ? (uint32_t)((uint64_t)(worker + 1) * total / np) : total;
+  if (threadIdx.x == 0) {
+    p->total = total;
+    p->np = np;
+    p->start = start;
+    p->end = end;
+    p->row = 0;
+    p->page = 0;
+  }
+  __syncthreads();
+  if (start < end && start >= before && start < before + mine) {
+    uint32_t at = before;
+    for (int r = r0; r < r1; ++r) {
+      const uint32_t n = (uint32_t)row_slots(v, r);
+      if (start < at + n) {
+        p->row = r;
+        p->page = (int)(start - at);
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+}
+
+// the segments of a worker's range, in order
+struct SegmentWalk {
+  uint32_t pos;
+  int row, page;                // next slot
+  __device__ __forceinline__ explicit SegmentWalk(const PagedPlan &p) : pos(p.start), row(p.row), page(p.page) {}
+  // slots [a, b) of row r, of n; part: partial slot or -1 for a whole row
+  __device__ __forceinline__ bool next(const PagedView &v, const PagedPlan &p, int worker, int *r, int *a, int *b,
+                                       int *part) {
+    while (pos < p.end) {
+      const int n = row_slots(v, row);
+      if (n == 0) {
+        ++row;
+        continue;
+      }
+      const int room = n - page, left = (int)(p.end - pos);
+      *r = row;
+      *a = page;
+      *b = page + (room < left ? room : left);
+      *part = (*a == 0 && *b == n) ? -1 : 2 * worker + (*a == 0 ? 1 : 0);
+      pos += (uint32_t)(*b - *a);
+      ++row;
+      page = 0;
+      return true;
+    }
+    return false;
+  }
+};
+
+// what the combine kernel has to join at this worker (one thread calls it)
+__device__ __forceinline__ int2 worker_info(const PagedView &v, const PagedPlan &p) {
+  if (p.start >= p.end || p.page == 0) return make_int2(-1, 0);
+  const int n = row_slots(v, p.row);
+  if ((uint32_t)(n - p.page) > p.end - p.start) return make_int2(-1, 0);      // the row goes on in the next worker
+  return make_int2(p.row, worker_of_slot(p.start - (uint32_t)p.page, p));
+}
+
+}  // namespace dsa

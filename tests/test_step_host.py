@@ -1,0 +1,193 @@
+"""Host-side checks of the serving step's calls (no GPU): sizes, and refusals before anything is enqueued."""
+import ctypes
+
+import pytest
+
+from sparse_attention_long_dsa_b200 import binding as B
+
+P = 1 << 24                                   # a 16-byte aligned address that is never read
+
+
+def _lib():
+    return B.load()
+
+
+def _err():
+    return _lib().dsa_last_error().decode()
+
+
+def test_workspace_sizes():
+    one = B.dsa_batch_workspace_size(B.DSA_OP_BATCH_EXTEND, 1)
+    assert one >= 256 and B.dsa_batch_workspace_size(B.DSA_OP_BATCH_RELEASE, 5000) >= one + 8 * 4999
+    for op, n in ((B.DSA_OP_TOPK, 4), (B.DSA_OP_BATCH_EXTEND, 0)):
+        with pytest.raises(B.DSAError) as e:
+            B.dsa_batch_workspace_size(op, n)
+        assert e.value.status == B.DSA_ERR_INVALID_ARG
+    b = _batch()
+    small, large = (B.dsa_workspace_size(B.DSA_OP_PAGED_DECODE, b, 0, h, 512) for h in (1, 128))
+    assert 256 < small < large
+    assert B.dsa_workspace_size(B.DSA_OP_QK_NORM_ROPE, b) == 256
+    assert B.dsa_workspace_size(B.DSA_OP_BATCH_EXTEND, b) == B.dsa_batch_workspace_size(B.DSA_OP_BATCH_EXTEND, b.num_seqs)
+    with pytest.raises(B.DSAError) as e:
+        B.dsa_workspace_size(B.DSA_OP_PAGED_DECODE, b, 0, 129, 512)
+    assert e.value.status == B.DSA_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------------------------------------ block tables
+def _extend(**kw):
+    d = dict(cached=P, add=2 * P, n=4, page=64, width=8, blocks=100, rows=4, free=3 * P, cap=100, count=4 * P,
+             table=5 * P, lens=P, cu=6 * P, slots=7 * P, pos=8 * P, left=4 * P, ws=9 * P, ws_bytes=1 << 20)
+    d.update(kw)
+    return _lib().dsa_batch_extend(*d.values(), None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(n=0), B.DSA_ERR_INVALID_ARG),
+    (dict(page=128), B.DSA_ERR_UNSUPPORTED),
+    (dict(width=0), B.DSA_ERR_INVALID_ARG),
+    (dict(width=1 << 26), B.DSA_ERR_UNSUPPORTED),
+    (dict(blocks=0), B.DSA_ERR_INVALID_ARG),
+    (dict(rows=-1), B.DSA_ERR_INVALID_ARG),
+    (dict(cached=None), B.DSA_ERR_INVALID_ARG),
+    (dict(free=None), B.DSA_ERR_INVALID_ARG),
+    (dict(cap=-1), B.DSA_ERR_INVALID_ARG),
+    (dict(slots=None), B.DSA_ERR_INVALID_ARG),
+    (dict(add=P), B.DSA_ERR_INVALID_ARG),              # new_lens is the cached lengths' array
+    (dict(ws_bytes=300), B.DSA_ERR_WORKSPACE),
+    (dict(ws=None), B.DSA_ERR_WORKSPACE),
+    (dict(ws=9 * P + 16), B.DSA_ERR_INVALID_ARG),
+])
+def test_extend_refusals(bad, status):
+    assert _extend(**bad) == status
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(n=0), B.DSA_ERR_INVALID_ARG),
+    (dict(page=32), B.DSA_ERR_UNSUPPORTED),
+    (dict(done=None), B.DSA_ERR_INVALID_ARG),
+    (dict(done=3 * P), B.DSA_ERR_INVALID_ARG),         # done is seq_lens
+    (dict(count=None), B.DSA_ERR_INVALID_ARG),
+    (dict(ws_bytes=0), B.DSA_ERR_WORKSPACE),
+])
+def test_release_refusals(bad, status):
+    d = dict(done=P, n=4, page=64, width=8, blocks=100, table=2 * P, lens=3 * P, free=4 * P, cap=100, count=5 * P, ws=6 * P,
+             ws_bytes=1 << 20)
+    d.update(bad)
+    assert _lib().dsa_batch_release(*d.values(), None) == status
+
+
+# ------------------------------------------------------------------------------------------------ norm and rotation
+def _part(**kw):
+    d = dict(x=P, out=2 * P, weight=3 * P, x_row_stride=576, x_head_stride=576, out_row_stride=576, out_head_stride=576,
+             out_rows=10, H=1, D=576, norm_off=0, norm_len=512, rope_off=512, rope_len=64, x_dt=B.DSA_BF16, w_dt=B.DSA_BF16,
+             out_dt=B.DSA_BF16, eps=1e-6)
+    d.update(kw)
+    return B.dsa_rope_part_t(**d)
+
+
+def _rope(parts, T=10, pos=4 * P, freq=5 * P, ws=6 * P, ws_bytes=256):
+    arr = (B.dsa_rope_part_t * len(parts))(*parts)
+    return _lib().dsa_qk_norm_rope(arr, len(parts), pos, T, freq, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(x=None), B.DSA_ERR_INVALID_ARG),
+    (dict(H=0), B.DSA_ERR_INVALID_ARG),
+    (dict(D=12), B.DSA_ERR_UNSUPPORTED),
+    (dict(D=1032), B.DSA_ERR_UNSUPPORTED),
+    (dict(x_dt=B.DSA_FP8_E4M3), B.DSA_ERR_UNSUPPORTED),
+    (dict(out_dt=7), B.DSA_ERR_UNSUPPORTED),
+    (dict(norm_len=584), B.DSA_ERR_INVALID_ARG),
+    (dict(norm_len=500), B.DSA_ERR_UNSUPPORTED),
+    (dict(weight=None), B.DSA_ERR_INVALID_ARG),
+    (dict(w_dt=B.DSA_FP8_E4M3), B.DSA_ERR_UNSUPPORTED),
+    (dict(eps=float("nan")), B.DSA_ERR_INVALID_ARG),
+    (dict(eps=-1.0), B.DSA_ERR_INVALID_ARG),
+    (dict(rope_off=520), B.DSA_ERR_INVALID_ARG),
+    (dict(rope_off=508), B.DSA_ERR_UNSUPPORTED),
+    (dict(rope_len=8), B.DSA_ERR_UNSUPPORTED),
+    (dict(rope_off=0, rope_len=272), B.DSA_ERR_UNSUPPORTED),
+    (dict(rope_style=2), B.DSA_ERR_INVALID_ARG),
+    (dict(out_scale=P), B.DSA_ERR_INVALID_ARG),        # a scale goes with e4m3
+    (dict(x_row_stride=-1), B.DSA_ERR_INVALID_ARG),
+    (dict(out_row_stride=512), B.DSA_ERR_INVALID_ARG),
+    (dict(H=2, out_head_stride=64), B.DSA_ERR_INVALID_ARG),
+    (dict(out_rows=9), B.DSA_ERR_INVALID_ARG),
+    (dict(slots=P, out_rows=0), B.DSA_ERR_INVALID_ARG),
+    (dict(slots=P + 4), B.DSA_ERR_INVALID_ARG),
+    (dict(x=P + 1), B.DSA_ERR_INVALID_ARG),
+])
+def test_rope_part_refusals(bad, status):
+    assert _rope([_part(), _part(**bad)]) == status
+
+
+def test_rope_call_refusals():
+    assert _rope([_part()], pos=None) == B.DSA_ERR_INVALID_ARG
+    assert _rope([_part()], freq=None) == B.DSA_ERR_INVALID_ARG
+    assert _rope([_part(), _part(rope_len=32)]) == B.DSA_ERR_INVALID_ARG and "differs" in _err()
+    assert _rope([_part()] * 5) == B.DSA_ERR_UNSUPPORTED
+    assert _rope([_part()], T=-1) == B.DSA_ERR_INVALID_ARG
+    assert _rope([_part()], ws_bytes=128) == B.DSA_ERR_WORKSPACE
+    assert _rope([_part(x=None)], T=0) == B.DSA_OK                       # empty: checked only for its sizes
+    assert _lib().dsa_qk_norm_rope(None, 1, P, 1, P, P, 256, None) == B.DSA_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------------------------------------ paged attention
+def _batch(**kw):
+    d = dict(num_seqs=3, page_size=64, num_blocks=40, max_blocks_per_seq=4, block_table=1 << 20, seq_lens=1 << 21,
+             cu_q=1 << 22, total_q=3, max_q_per_seq=1, max_seq_len=200)
+    d.update(kw)
+    return B.dsa_batch_t(**d)
+
+
+def _attn(batch=None, **kw):
+    d = dict(q=P, dt=B.DSA_BF16, kv=2 * P, v=None, H=128, Dqk=576, Dv=512, scale=0.1, pages=None, kb=0)
+    d.update(kw)
+    b = batch or _batch()
+    ws = kw.pop("ws_bytes", 1 << 30)
+    d.pop("ws_bytes", None)
+    return _lib().dsa_paged_attn_decode(*d.values(), ctypes.byref(b), 3 * P, None, 4 * P, ws, None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(q=None), B.DSA_ERR_INVALID_ARG),
+    (dict(H=0), B.DSA_ERR_UNSUPPORTED),
+    (dict(H=129), B.DSA_ERR_UNSUPPORTED),
+    (dict(Dqk=512), B.DSA_ERR_UNSUPPORTED),
+    (dict(v=P), B.DSA_ERR_UNSUPPORTED),
+    (dict(dt=B.DSA_FP8_E4M3), B.DSA_ERR_UNSUPPORTED),
+    (dict(dt=B.DSA_F32, H=17, Dqk=64, Dv=64, v=P), B.DSA_ERR_UNSUPPORTED),
+    (dict(dt=B.DSA_F32, H=4, Dqk=64, Dv=64), B.DSA_ERR_UNSUPPORTED),      # f32 needs its own value cache
+    (dict(scale=0.0), B.DSA_ERR_INVALID_ARG),
+    (dict(scale=float("nan")), B.DSA_ERR_INVALID_ARG),
+    (dict(kb=4), B.DSA_ERR_INVALID_ARG),
+    (dict(pages=P, kb=0), B.DSA_ERR_INVALID_ARG),
+    (dict(pages=P, kb=1 << 30), B.DSA_ERR_UNSUPPORTED),
+    (dict(kv=2 * P + 8), B.DSA_ERR_INVALID_ARG),
+    (dict(ws_bytes=1024), B.DSA_ERR_WORKSPACE),
+])
+def test_paged_attention_refusals(bad, status):
+    assert _attn(**bad) == status
+
+
+def test_paged_attention_batch_refusals():
+    assert _attn(_batch(total_q=4, max_q_per_seq=2)) == B.DSA_ERR_INVALID_ARG and "one query row" in _err()
+    assert _attn(_batch(page_size=32)) == B.DSA_ERR_UNSUPPORTED
+    assert _attn(_batch(num_blocks=1 << 25)) == B.DSA_ERR_UNSUPPORTED
+    assert _attn(_batch(total_q=0, max_q_per_seq=0), q=None) == B.DSA_OK
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    t = torch.zeros(4, 64)
+    with pytest.raises(B.DSAError) as e:
+        B.rope_part(t, t)
+    assert e.value.status == B.DSA_ERR_INVALID_ARG
+    i = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(B.DSAError) as e:
+        B.dsa_batch_extend(i, i, 64, 4, 4, i, i, torch.zeros(4, 2, dtype=torch.int32), i, torch.zeros(5, dtype=torch.int32), i,
+                           i, i, 1 << 24, 1 << 20)
+    assert e.value.status == B.DSA_ERR_INVALID_ARG
+    with pytest.raises(B.DSAError) as e:
+        B.dsa_qk_norm_rope([], None, None, 1 << 24, 256)
+    assert e.value.status == B.DSA_ERR_UNSUPPORTED
