@@ -1,0 +1,586 @@
+// One-token attention over the paged latent cache on tcgen05 tensor cores, one CTA pair (cluster of 2) per worker.
+//
+//   z[h, s] = scale * q[h, :] . K[s],   out[h, :] = sum_s softmax_s(z[h, :]) V[s],   V[s] = first 512 of the 576 entries
+// for up to 128 heads of the row, over the tokens of every page of the sequence or of a list of pages ("Engineering
+// Practices for Day-0 Adaptation of Million-Token Context Models on Domestic AI Chips", Four Key Layers 3: decode
+// prefetches the next KV block while the current one is computed, partial results are merged by a cross-block reduction).
+//
+// A token costs 1152 bytes of HBM and 2 x 128 x 1088 products whatever the number of heads (missing heads are zero rows of
+// q): 0.176 ns of copy bandwidth against 0.085 ns of a pair's tensor time over 74 pairs, so the kernel is built to keep the
+// copies running.  Work split of a pair (rank r = 0, 1), one page of 64 tokens at a time, over the flat range of page slots
+// that paged.cuh gives it:
+//   * resolve: one warp per CTA walks the slots (32 table entries per load) and publishes the pages that hold tokens to the
+//              other roles through a ring: physical row, tokens, row, first / last of its segment;
+//   * keys   : each CTA copies ITS 32 tokens of the page, all 576 entries, into one of three buffers [9 blocks][32 tokens]
+//              [128 B] by nine tiled TMA copies (a page is contiguous).  The last page of a sequence comes by gather4
+//              instead, whose rows past the sequence are zero-filled: nothing stale reaches the tensor cores;
+//   * QK^T   : M = 128 heads (64 per CTA), N = 64 tokens (32 from each CTA), K = 576;
+//   * values : each CTA needs 256 of the 512 value entries of all 64 tokens: the peer's 32 tokens' half (16 KB, an L2 hit)
+//              is copied over the blocks that QK^T no longer needs, as soon as it has run;
+//   * softmax: 4 warps per CTA, one (head, 32-token half) per thread; O is rescaled in TMEM only when the running maximum
+//              grows by more than 2^8 (exact: the final division uses the same reference);
+//   * P V    : two N = 256 MMAs over K = 64 tokens; O (64 heads x 512 fp32 per CTA) stays in TMEM.
+// P is rounded to bf16 for P V, as the tensor cores take it; the sum l keeps the unrounded weights in fp32.
+#include <algorithm>
+#include <atomic>
+
+#include "paged.cuh"
+#include "tc.cuh"
+
+namespace dsa {
+
+constexpr int kPtD = 576, kPtDv = 512;
+constexpr int kPtHalf = kPage / 2;
+constexpr int kPtNBuf = 3;
+constexpr int kPtRing = 8;                         // published pages in flight
+constexpr int kPtThreads = 256;                    // softmax x 4, keys, MMA, resolve, values
+constexpr int kPtWarpKeys = 4, kPtWarpMMA = 5, kPtWarpResolve = 6, kPtWarpValues = 7;
+constexpr uint32_t kPtBlk = kPtHalf * 128;         // one 64-entry block of a CTA's 32 tokens: 4 KB
+constexpr uint32_t kPtBuf = 9 * kPtBlk;
+constexpr uint32_t kPtQ = 9 * 8192;
+constexpr uint32_t kPtP = 8192;                    // [64 heads][64 tokens] bf16
+constexpr uint32_t kPtTmemO = 0, kPtTmemS = 256;
+constexpr float kPtRescale = 8.0f;
+constexpr int kPtFirst = 1, kPtLast = 2, kPtEmpty = 4, kPtEnd = 8;
+
+struct PtSmem {
+  uint64_t buf_full[kPtNBuf];       // rank 0: bytes of both CTAs' tokens
+  uint64_t buf_empty[kPtNBuf];      // MMA commit to both CTAs after P V
+  uint64_t v_full[kPtNBuf];         // rank 0: bytes of both CTAs' peer values
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t o_empty, drain;
+  uint64_t ent_full[kPtRing], ent_empty[kPtRing];
+  uint32_t tmem_base;
+  int abort;
+  int4 ent[kPtRing];                // physical row, tokens, row, flags | (part + 1) << 8
+  float xm[2][128];
+  float xl[128];
+  uint32_t tmp[33];
+  PagedPlan plan;
+};
+
+struct PtArgs {
+  PagedView view;
+  PagedOut o;
+  int H;
+  float scale_log2;
+  int min_slots;
+};
+
+__device__ __forceinline__ void pt_load_3d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+// true if any of the 128 softmax threads says so
+__device__ __forceinline__ bool pt_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 3, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+// 32 tokens of a page, from token t0 on, `n` 64-entry blocks: column block src + i to dst + i * 4 KB.  Whole warp.
+__device__ __forceinline__ void pt_copy(const CUtensorMap *tiles, const CUtensorMap *rows, int lane, int phys, int ntok, int t0,
+                                        int oob, int src, int n, uint32_t dst, uint32_t bar) {
+  if (ntok == kPage) {
+    if (lane < n) tc::tma_load_2d_pair(dst + lane * kPtBlk, tiles, (src + lane) * 64, phys + t0, bar);
+  } else if (lane < kPtHalf / 4) {
+    int r4[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = t0 + 4 * lane + e;
+      r4[e] = t < ntok ? phys + t : oob;
+    }
+    for (int i = 0; i < n; ++i)
+      tc::tma_gather4_pair(dst + i * kPtBlk + 4 * lane * 128, rows, (src + i) * 64, r4[0], r4[1], r4[2], r4[3], bar);
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
+    paged_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_tiles,
+                     const __grid_constant__ CUtensorMap tm_rows, const PtArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *sQ = smem;                              // [9 blocks][64 heads][128 B]
+  uint8_t *sBuf = sQ + kPtQ;                       // 3 x [9 blocks][32 tokens][128 B]
+  uint8_t *sP = sBuf + kPtNBuf * kPtBuf;           // 2 x P; epilogue staging
+  PtSmem *S = (PtSmem *)(sP + 2 * kPtP);
+
+  const uint32_t rank = tc::cluster_ctarank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPtNBuf; ++i) {
+      tc::mbar_init(tc::smem_u32(&S->buf_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&S->buf_empty[i]), 1);
+      tc::mbar_init(tc::smem_u32(&S->v_full[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tc::smem_u32(&S->s_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&S->p_full[i]), 8);
+      tc::mbar_init(tc::smem_u32(&S->pv_done[i]), 1);
+    }
+    tc::mbar_init(tc::smem_u32(&S->q_full), 1);
+    tc::mbar_init(tc::smem_u32(&S->q_empty), 1);
+    tc::mbar_init(tc::smem_u32(&S->o_empty), 8);
+    tc::mbar_init(tc::smem_u32(&S->drain), 1);
+    for (int i = 0; i < kPtRing; ++i) {
+      tc::mbar_init(tc::smem_u32(&S->ent_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&S->ent_empty[i]), rank == 0 ? 7 : 6);   // softmax x 4, keys, values, MMA (rank 0)
+    }
+    S->abort = 0;
+    tc::fence_barrier_init();
+    tc::prefetch_tmap(&tm_q);
+    tc::prefetch_tmap(&tm_tiles);
+    tc::prefetch_tmap(&tm_rows);
+  }
+  if (warp == kPtWarpMMA) {
+    tc::tmem_alloc2(tc::smem_u32(&S->tmem_base), 512);
+    tc::tmem_relinquish2();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = S->tmem_base;
+  volatile int *abort = &S->abort;
+  uint32_t *status = a.o.status;
+  // inputs come from earlier work on the stream
+  pdl_wait();
+  pdl_trigger();
+  plan_pages(a.view, pair, npairs, a.min_slots, S->tmp, &S->plan);
+
+  // next entry of the ring, for a whole warp: false ends the role (the end of the work, or a wait that ran out)
+  auto next_entry = [&](uint32_t &ec, int4 *e) -> bool {
+    const uint32_t slot = ec % kPtRing;
+    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&S->ent_full[slot]), (ec / kPtRing) & 1u, abort, status));
+    if (!ok) return false;
+    *e = S->ent[slot];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(tc::smem_u32(&S->ent_empty[slot]));
+    ++ec;
+    return true;
+  };
+
+  if (warp == kPtWarpResolve) {
+    // ====================================================================== resolve
+    if (lane == 0 && rank == 0) a.o.info[pair] = worker_info(a.view, S->plan);
+    uint32_t ec = 0;
+    auto push = [&](int phys, int ntok, int row, int info) {
+      const uint32_t slot = ec % kPtRing;
+      const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&S->ent_empty[slot]), ((ec / kPtRing) & 1u) ^ 1u, abort,
+                                                            status));
+      if (lane == 0 && ok) {
+        S->ent[slot] = make_int4(phys, ntok, row, info);
+        tc::mbar_arrive(tc::smem_u32(&S->ent_full[slot]));
+      }
+      __syncwarp();
+      ++ec;
+      return ok;
+    };
+    SegmentWalk walk(S->plan);
+    int row, sa, sb, part;
+    bool ok = true;
+    while (ok && walk.next(a.view, S->plan, pair, &row, &sa, &sb, &part)) {
+      const int n = row_tokens(a.view, row, status);
+      const int tag = (part + 1) << 8;
+      int flags = kPtFirst, h_phys = 0, h_ntok = 0;        // one page is held back until it is known whether another follows
+      for (int s0 = sa; s0 < sb && ok; s0 += 32) {
+        int blk = 0, nt = 0;
+        if (s0 + lane < sb) nt = slot_tokens(a.view, row, n, s0 + lane, &blk, status);
+        uint32_t have = __ballot_sync(0xffffffffu, nt > 0);
+        while (have && ok) {
+          const int l = __ffs(have) - 1;
+          have &= have - 1;
+          if (h_ntok) {
+            ok = push(h_phys, h_ntok, row, flags | tag);
+            flags = 0;
+          }
+          h_phys = __shfl_sync(0xffffffffu, blk, l) * kPage;
+          h_ntok = __shfl_sync(0xffffffffu, nt, l);
+        }
+      }
+      if (ok) ok = push(h_phys, h_ntok, row, (h_ntok ? flags | kPtLast : kPtEmpty) | tag);
+    }
+    if (ok) push(0, 0, 0, kPtEnd);
+  } else if (warp == kPtWarpKeys) {
+    // ====================================================================== keys and q
+    const int oob = a.view.num_blocks * kPage;             // a row outside the map: zero-filled
+    const uint32_t buf_full_r0 = tc::map_to_rank(tc::smem_u32(&S->buf_full[0]), 0);
+    const uint32_t q_full_r0 = tc::map_to_rank(tc::smem_u32(&S->q_full), 0);
+    uint32_t ec = 0, c = 0, v = 0;
+    int4 e;
+    while (next_entry(ec, &e)) {
+      if (e.w & kPtEnd) break;
+      if (e.w & kPtEmpty) continue;
+      const uint32_t b = c % kPtNBuf;
+      if (!tc::mbar_wait_cl_w(tc::smem_u32(&S->buf_empty[b]), ((c / kPtNBuf) & 1u) ^ 1u, abort, status)) break;
+      if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->buf_full[b]), 2u * kPtBuf);
+      __syncwarp();
+      pt_copy(&tm_tiles, &tm_rows, lane, e.x, e.y, kPtHalf * (int)rank, oob, 0, 9, tc::smem_u32(sBuf + b * kPtBuf),
+              buf_full_r0 + b * 8);
+      if (e.w & kPtFirst) {
+        // q is overwritten once the previous segment's last QK^T has run
+        if (v > 0 && !tc::mbar_wait_cl_w(tc::smem_u32(&S->q_empty), (v - 1) & 1u, abort, status)) break;
+        if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->q_full), 2u * kPtQ);
+        __syncwarp();
+        if (lane < 9) pt_load_3d_pair(tc::smem_u32(sQ + lane * 8192), &tm_q, lane * 64, 64 * (int)rank, e.z, q_full_r0);
+        ++v;
+      }
+      ++c;
+    }
+  } else if (warp == kPtWarpValues) {
+    // ====================================================================== the peer's values
+    const int oob = a.view.num_blocks * kPage;
+    const uint32_t v_full_r0 = tc::map_to_rank(tc::smem_u32(&S->v_full[0]), 0);
+    const int dst = rank == 0 ? 4 : 0, src = rank == 0 ? 0 : 4;
+    uint32_t ec = 0, c = 0;
+    int4 e;
+    while (next_entry(ec, &e)) {
+      if (e.w & kPtEnd) break;
+      if (e.w & kPtEmpty) continue;
+      const uint32_t b = c % kPtNBuf;
+      // QK^T of this page has read the buffers
+      if (!tc::mbar_wait_cl_w(tc::smem_u32(&S->s_full[c & 1u]), (c >> 1) & 1u, abort, status)) break;
+      if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->v_full[b]), 2u * 4u * kPtBlk);
+      __syncwarp();
+      pt_copy(&tm_tiles, &tm_rows, lane, e.x, e.y, kPtHalf * (int)(rank ^ 1u), oob, src, 4,
+              tc::smem_u32(sBuf + b * kPtBuf + dst * kPtBlk), v_full_r0 + b * 8);
+      ++c;
+    }
+  } else if (warp == kPtWarpMMA) {
+    // ====================================================================== MMA issuer (rank 0, whole warp)
+    if (rank == 0) {
+      const uint32_t idesc_qk = tc::make_idesc(1, 1, 128, kPage, false, false);
+      const uint32_t idesc_pv = tc::make_idesc(1, 1, 128, 256, false, true);
+      const uint16_t both = 3;
+      const uint64_t q_desc = tc::desc_sw128(tc::smem_u32(sQ), 1024);
+      const uint64_t p_desc = tc::desc_sw128(tc::smem_u32(sP), 1024);
+      const uint64_t kv_desc = tc::desc_sw128(tc::smem_u32(sBuf), 1024);
+      const uint64_t v_desc = tc::desc_sw128_lbo(tc::smem_u32(sBuf), kPtBlk, 1024);
+      uint32_t ec = 0, c = 0, v = 0;
+      auto pv = [&](uint32_t cc, bool first) -> bool {
+        const uint32_t b = cc % kPtNBuf, pb = cc & 1u;
+        if (!tc::mbar_wait_cl_w(tc::smem_u32(&S->p_full[pb]), (cc >> 1) & 1u, abort, status)) return false;
+        if (!tc::mbar_wait_cl_w(tc::smem_u32(&S->v_full[b]), (cc / kPtNBuf) & 1u, abort, status)) return false;
+        if (first && v > 0 && !tc::mbar_wait_cl_w(tc::smem_u32(&S->o_empty), (v - 1) & 1u, abort, status)) return false;
+        tc::fence_after_sync();
+        const uint64_t pa = p_desc + ((pb * kPtP) >> 4), vb = v_desc + ((b * kPtBuf) >> 4);
+        // K steps of 16 tokens: token half (4 blocks apart) x two steps of 16 rows
+        constexpr int kS = (16 * 128) >> 4, kH = (4 * kPtBlk) >> 4;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          tc::mma_bf16_pair_x4_w<kS, kH, kH + kS>(tmem + kPtTmemO + 128 * p, pa, vb + ((2 * p * kPtBlk) >> 4), idesc_pv,
+                                                  first ? 0u : 1u);
+        tc::mma_commit_pair_w(tc::smem_u32(&S->buf_empty[b]), both);
+        tc::mma_commit_pair_w(tc::smem_u32(&S->pv_done[pb]), both);
+        return true;
+      };
+      int4 e;
+      bool prev_first = false;
+      while (next_entry(ec, &e)) {
+        if (e.w & kPtEnd) break;
+        if (e.w & kPtEmpty) continue;
+        const bool first = e.w & kPtFirst, last = e.w & kPtLast;
+        const uint32_t b = c % kPtNBuf;
+        if (first && !tc::mbar_wait_cl_w(tc::smem_u32(&S->q_full), v & 1u, abort, status)) break;
+        if (!tc::mbar_wait_cl_w(tc::smem_u32(&S->buf_full[b]), (c / kPtNBuf) & 1u, abort, status)) break;
+        tc::fence_after_sync();
+        tc::mma_qk36_pair_w<kPtBlk>(tmem + kPtTmemS + kPtHalf * (c & 1u), q_desc, kv_desc + ((b * kPtBuf) >> 4), idesc_qk);
+        tc::mma_commit_pair_w(tc::smem_u32(&S->s_full[c & 1u]), both);
+        if (last) tc::mma_commit_pair_w(tc::smem_u32(&S->q_empty), both);
+        if (!first && !pv(c - 1, prev_first)) break;
+        prev_first = first;
+        if (last) {
+          if (!pv(c, first)) break;
+          ++v;
+        }
+        ++c;
+      }
+      tc::mma_commit_pair_local_w(tc::smem_u32(&S->drain));
+      volatile int no_abort = 0;
+      __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&S->drain), 0, &no_abort, status));
+    }
+  } else {
+    // ====================================================================== softmax + epilogue (warps 0-3)
+    // The four warps leave the loop together (pt_any): they hold named barriers.
+    const int L = threadIdx.x;                     // TMEM lane
+    const int h = L & 63, half = L >> 6;
+    const int head = 64 * (int)rank + h;
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const uint32_t p_full_r0 = tc::map_to_rank(tc::smem_u32(&S->p_full[0]), 0);
+    const uint32_t o_empty_r0 = tc::map_to_rank(tc::smem_u32(&S->o_empty), 0);
+    __nv_bfloat16 *out = (__nv_bfloat16 *)a.o.out;
+    float m_run = -INFINITY, l_run = 0.f;
+    uint32_t ec = 0, c = 0;
+    int4 e;
+    for (;;) {
+      if (pt_any(!next_entry(ec, &e)) || (e.w & kPtEnd)) break;
+      const int row = e.z, part = (e.w >> 8) - 1;
+      if (e.w & kPtEmpty) {                        // no page of the segment holds a token
+        if (head < a.H) {
+          if (part < 0) {
+            __nv_bfloat16 *o = out + ((int64_t)row * a.H + head) * kPtDv + 256 * half;
+            for (int i = 0; i < 256; i += 8) *reinterpret_cast<uint4 *>(o + i) = make_uint4(0, 0, 0, 0);
+            if (a.o.lse && half == 0) a.o.lse[(int64_t)row * a.H + head] = -INFINITY;
+          } else {
+            float *o = a.o.part_o + ((int64_t)part * a.H + head) * kPtDv + 256 * half;
+            for (int i = 0; i < 256; i += 4) *reinterpret_cast<float4 *>(o + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (half == 0) a.o.part_lse[(int64_t)part * a.H + head] = -INFINITY;
+          }
+        }
+        continue;
+      }
+      const bool first = e.w & kPtFirst;
+      if (first) {
+        m_run = -INFINITY;
+        l_run = 0.f;
+      }
+      const int mine = e.y - kPtHalf * half;       // tokens of this thread's half
+      const bool have_s =
+          __all_sync(0xffffffffu, tc::mbar_wait_cl(tc::smem_u32(&S->s_full[c & 1u]), (c >> 1) & 1u, abort, status));
+      tc::fence_after_sync();
+      float sv[kPtHalf];
+      tc::tmem_ld32(tmem + lane_base + kPtTmemS + kPtHalf * (c & 1u), sv);
+      tc::tmem_wait_ld();
+      const int valid = have_s ? mine : 0;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kPtHalf; ++i) {
+        sv[i] = i < valid ? sv[i] * a.scale_log2 : -INFINITY;
+        mx = fmaxf(mx, sv[i]);
+      }
+      const float mloc = fmaxf(m_run, mx);
+      S->xm[c & 1u][L] = mloc;
+      tc::named_bar_sync(2, 128);
+      const float m_new = fmaxf(mloc, S->xm[c & 1u][L ^ 64]);
+      bool pv_ok = true;
+      if (first) {
+        m_run = m_new;
+      } else {
+        // TMEM accesses are warp-collective: the warp rescales if any of its rows needs it, rows that do not keep their
+        // reference (alpha = 1).  P V of the previous page must have finished before O is touched.
+        const bool want = m_new > m_run + kPtRescale;
+        if (__any_sync(0xffffffffu, want)) {
+          const uint32_t cp = c - 1;
+          pv_ok = __all_sync(0xffffffffu, tc::mbar_wait_cl(tc::smem_u32(&S->pv_done[cp & 1u]), (cp >> 1) & 1u, abort, status));
+          tc::fence_after_sync();
+          const float alpha = want ? tc::ex2(m_run - m_new) : 1.f;
+          if (pv_ok) {
+            for (int cc = 0; cc < 8; ++cc) {
+              float ov[32];
+              tc::tmem_ld32(tmem + lane_base + kPtTmemO + 32 * cc, ov);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) ov[i] *= alpha;
+              tc::tmem_st32(tmem + lane_base + kPtTmemO + 32 * cc, ov);
+            }
+            tc::tmem_wait_st();
+          }
+          if (want) {
+            l_run *= alpha;
+            m_run = m_new;
+          }
+        }
+      }
+      // this P buffer was last read by P V of page c - 2
+      if (c >= 2)
+        pv_ok = __all_sync(0xffffffffu, tc::mbar_wait_cl(tc::smem_u32(&S->pv_done[c & 1u]), ((c >> 1) & 1u) ^ 1u, abort, status)) &&
+                pv_ok;
+      // P = exp2(z - m) in bf16 into the 128-byte-swizzled A operand; masked tokens hold -inf and give 0
+      if (pv_ok) {
+        const float m_use = m_run == -INFINITY ? 0.f : m_run;
+        uint8_t *pbuf = sP + (c & 1u) * kPtP + h * 128;
+        float lsum = 0.f;
+#pragma unroll
+        for (int q8 = 0; q8 < kPtHalf / 8; ++q8) {
+          uint32_t w4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t0 = 8 * q8 + 2 * i;
+            const float p0 = tc::ex2(sv[t0] - m_use), p1 = tc::ex2(sv[t0 + 1] - m_use);
+            lsum += p0 + p1;
+            const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+            w4[i] = *reinterpret_cast<const uint32_t *>(&pb);
+          }
+          const int kc = (kPtHalf / 8) * half + q8;
+          *reinterpret_cast<uint4 *>(pbuf + ((kc ^ (h & 7)) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        }
+        l_run += lsum;
+      }
+      tc::fence_proxy_async();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) tc::mbar_arrive(tc::smem_u32(&S->p_full[c & 1u]));
+        else tc::mbar_arrive_remote(p_full_r0 + (c & 1u) * 8);
+      }
+      ++c;
+      if (!(e.w & kPtLast)) continue;
+
+      // ---- epilogue: wait for the last P V, normalise, store through a per-warp staging tile
+      const uint32_t cl = c - 1;
+      const bool o_ok =
+          __all_sync(0xffffffffu, tc::mbar_wait_cl(tc::smem_u32(&S->pv_done[cl & 1u]), (cl >> 1) & 1u, abort, status));
+      tc::fence_after_sync();
+      S->xl[L] = l_run;
+      tc::named_bar_sync(2, 128);
+      const float l_tot = l_run + S->xl[L ^ 64];
+      const float inv = l_tot != 0.f ? 1.f / l_tot : 0.f;
+      if (o_ok) {
+        // both P buffers are free once the last P V finished: each warp stages a 32 x 32 fp32 tile (row = lane, 16-byte
+        // group j at j ^ (row & 7)) and writes whole 128-byte row segments
+        float *stg = reinterpret_cast<float *>(sP) + warp * 1024;
+        const int head0 = 64 * (int)rank + 32 * (warp & 1), col0 = 256 * (warp >> 1);
+        if (head0 < a.H) {
+          for (int cc = 0; cc < 8; ++cc) {
+            float ov[32];
+            tc::tmem_ld32(tmem + lane_base + kPtTmemO + 32 * cc, ov);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4 *>(stg + lane * 32 + 4 * (j ^ (lane & 7))) =
+                  make_float4(ov[4 * j] * inv, ov[4 * j + 1] * inv, ov[4 * j + 2] * inv, ov[4 * j + 3] * inv);
+            __syncwarp();
+            if (part < 0) {
+#pragma unroll
+              for (int it = 0; it < 4; ++it) {
+                const int r = 8 * it + (lane >> 2), j0 = 2 * (lane & 3);
+                const float4 f0 = *reinterpret_cast<const float4 *>(stg + r * 32 + 4 * (j0 ^ (r & 7)));
+                const float4 f1 = *reinterpret_cast<const float4 *>(stg + r * 32 + 4 * ((j0 + 1) ^ (r & 7)));
+                const __nv_bfloat162 b0 = __floats2bfloat162_rn(f0.x, f0.y), b1 = __floats2bfloat162_rn(f0.z, f0.w);
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(f1.x, f1.y), b3 = __floats2bfloat162_rn(f1.z, f1.w);
+                uint4 w;
+                w.x = *reinterpret_cast<const uint32_t *>(&b0);
+                w.y = *reinterpret_cast<const uint32_t *>(&b1);
+                w.z = *reinterpret_cast<const uint32_t *>(&b2);
+                w.w = *reinterpret_cast<const uint32_t *>(&b3);
+                if (head0 + r < a.H)
+                  *reinterpret_cast<uint4 *>(out + ((int64_t)row * a.H + head0 + r) * kPtDv + col0 + 32 * cc + 4 * j0) = w;
+              }
+            } else {
+#pragma unroll
+              for (int it = 0; it < 8; ++it) {
+                const int r = 4 * it + (lane >> 3), j = lane & 7;
+                if (head0 + r < a.H)
+                  *reinterpret_cast<float4 *>(a.o.part_o + ((int64_t)part * a.H + head0 + r) * kPtDv + col0 + 32 * cc + 4 * j) =
+                      *reinterpret_cast<const float4 *>(stg + r * 32 + 4 * (j ^ (r & 7)));
+              }
+            }
+            __syncwarp();
+          }
+        }
+        if (half == 0 && head < a.H) {
+          const float lse = l_tot != 0.f ? (m_run + __log2f(l_tot)) * 0.69314718055994531f : -INFINITY;
+          if (part >= 0) a.o.part_lse[(int64_t)part * a.H + head] = lse;
+          else if (a.o.lse) a.o.lse[(int64_t)row * a.H + head] = lse;
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) tc::mbar_arrive(tc::smem_u32(&S->o_empty));
+        else tc::mbar_arrive_remote(o_empty_r0);
+      }
+    }
+  }
+
+  // ---- teardown: every role is done; MMAs drained; the peer done with our barriers, buffers and TMEM
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();
+  if (warp == kPtWarpMMA) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc2(tmem, 512);
+  }
+  // rows without a cached token: zeros, and -inf for the log-sum-exp
+  for (int r = blockIdx.x; r < a.view.T; r += gridDim.x) {
+    if (row_slots(a.view, r) > 0) continue;
+    uint4 *o = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o.out + (int64_t)r * a.H * kPtDv);
+    for (int i = threadIdx.x; i < a.H * kPtDv / 8; i += kPtThreads) o[i] = make_uint4(0, 0, 0, 0);
+    if (a.o.lse)
+      for (int i = threadIdx.x; i < a.H; i += kPtThreads) a.o.lse[(int64_t)r * a.H + i] = -INFINITY;
+  }
+}
+
+// ------------------------------------------------------------------------------------------------ host
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled_fn();
+
+static bool pt_map(CUtensorMap *m, const void *base, uint32_t rank, uint64_t d1, uint64_t d2, uint32_t box1) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)kPtD, d1, d2};
+  cuuint64_t strides[2] = {(cuuint64_t)kPtD * 2, (cuuint64_t)kPtD * 2 * d1};
+  cuuint32_t box[3] = {64, box1, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The main kernel of the latent cache; returns the workers (CTA pairs) through *workers for the join.
+dsa_status_t paged_mla_launch(const void *q, const void *kv, int H, float softmax_scale, const PagedView &view,
+                              const PagedOut &o, int max_workers, cudaStream_t stream, int num_sms, int *workers) {
+  PtArgs a{view, o, H, softmax_scale * 1.4426950408889634f, 2};
+  CUtensorMap tm_q, tm_tiles, tm_rows;
+  const uint64_t rows = (uint64_t)view.num_blocks * kPage;
+  if (!pt_map(&tm_q, q, 3, (uint64_t)H, (uint64_t)view.T, 64) || !pt_map(&tm_tiles, kv, 2, rows, 1, kPtHalf) ||
+      !pt_map(&tm_rows, kv, 2, rows, 1, 1)) {
+    set_error("paged attention: cuTensorMapEncodeTiled failed");
+    return DSA_ERR_CUDA;
+  }
+  const size_t smem = 1024 + kPtQ + kPtNBuf * kPtBuf + 2 * kPtP + sizeof(PtSmem);
+  // as many CTA pairs as can be resident at once, found once per device (threads that race on the first call
+  // compute the same number)
+  static std::atomic<int> resident[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    set_error("no current CUDA device");
+    return DSA_ERR_CUDA;
+  }
+  int pairs = resident[dev].load(std::memory_order_relaxed);
+  if (pairs == 0) {
+    if (cudaFuncSetAttribute(paged_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+      set_error("paged attention: %s", cudaGetErrorString(cudaGetLastError()));
+      return DSA_ERR_CUDA;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(num_sms & ~1);
+    cfg.blockDim = dim3(kPtThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, paged_mla_kernel, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = num_sms / 2;
+    }
+    pairs = std::max(1, std::min(n, num_sms / 2));
+    resident[dev].store(pairs, std::memory_order_relaxed);
+  }
+  *workers = std::min(pairs, max_workers);
+  DSA_LAUNCH_PDL("paged_mla_kernel", paged_mla_kernel, dim3(2 * *workers), dim3(kPtThreads), smem, stream, tm_q, tm_tiles,
+                 tm_rows, a);
+  return DSA_OK;
+}
+
+}  // namespace dsa
