@@ -33,8 +33,9 @@ constexpr int kPtD = 576, kPtDv = 512;
 constexpr int kPtHalf = kPage / 2;
 constexpr int kPtNBuf = 3;
 constexpr int kPtRing = 8;                         // published pages in flight
-constexpr int kPtThreads = 256;                    // softmax x 4, keys, MMA, resolve, values
-constexpr int kPtWarpKeys = 4, kPtWarpMMA = 5, kPtWarpResolve = 6, kPtWarpValues = 7;
+constexpr int kPtThreads = 384;                    // softmax x 8, keys, MMA, resolve, values
+constexpr int kPtSoftmax = 256;
+constexpr int kPtWarpKeys = 8, kPtWarpMMA = 9, kPtWarpResolve = 10, kPtWarpValues = 11;
 constexpr uint32_t kPtBlk = kPtHalf * 128;         // one 64-entry block of a CTA's 32 tokens: 4 KB
 constexpr uint32_t kPtBuf = 9 * kPtBlk;
 constexpr uint32_t kPtQ = 9 * 8192;
@@ -54,8 +55,8 @@ struct PtSmem {
   uint32_t tmem_base;
   int abort;
   int4 ent[kPtRing];                // physical row, tokens, row, flags | (part + 1) << 8
-  float xm[2][128];
-  float xl[128];
+  float xm[2][kPtSoftmax];
+  float xl[kPtSoftmax];
   uint32_t tmp[33];
   PagedPlan plan;
 };
@@ -63,6 +64,7 @@ struct PtSmem {
 struct PtArgs {
   PagedView view;
   PagedOut o;
+  const __nv_bfloat16 *kv;
   int H;
   float scale_log2;
   int min_slots;
@@ -75,18 +77,46 @@ __device__ __forceinline__ void pt_load_3d_pair(uint32_t dst, const CUtensorMap 
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-// true if any of the 128 softmax threads says so
+// true if any of the softmax threads says so
 __device__ __forceinline__ bool pt_any(bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 3, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, 3, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "n"(kPtSoftmax)
       : "memory");
   return r != 0;
+}
+
+__device__ __forceinline__ bool pt_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ void pt_mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// 16 consecutive columns of this thread's TMEM lane
+__device__ __forceinline__ void pt_tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // 32 tokens of a page, from token t0 on, `n` 64-entry blocks: column block src + i to dst + i * 4 KB.  Whole warp.
@@ -128,16 +158,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(tc::smem_u32(&S->s_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&S->p_full[i]), 8);
+      tc::mbar_init(tc::smem_u32(&S->p_full[i]), 2 * kPtSoftmax / 32);
       tc::mbar_init(tc::smem_u32(&S->pv_done[i]), 1);
     }
     tc::mbar_init(tc::smem_u32(&S->q_full), 1);
     tc::mbar_init(tc::smem_u32(&S->q_empty), 1);
-    tc::mbar_init(tc::smem_u32(&S->o_empty), 8);
+    tc::mbar_init(tc::smem_u32(&S->o_empty), 2 * kPtSoftmax / 32);
     tc::mbar_init(tc::smem_u32(&S->drain), 1);
     for (int i = 0; i < kPtRing; ++i) {
       tc::mbar_init(tc::smem_u32(&S->ent_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&S->ent_empty[i]), rank == 0 ? 7 : 6);   // softmax x 4, keys, values, MMA (rank 0)
+      tc::mbar_init(tc::smem_u32(&S->ent_empty[i]), kPtSoftmax / 32 + (rank == 0 ? 3 : 2));   // keys, values, MMA (rank 0)
     }
     S->abort = 0;
     tc::fence_barrier_init();
@@ -184,6 +214,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       if (lane == 0 && ok) {
         S->ent[slot] = make_int4(phys, ntok, row, info);
         tc::mbar_arrive(tc::smem_u32(&S->ent_full[slot]));
+        const int t0 = kPtHalf * (int)rank, n = min(kPtHalf, ntok - t0);
+        if (n > 0) tc::prefetch_l2(a.kv + ((int64_t)phys + t0) * kPtD, (uint32_t)n * kPtD * 2);
       }
       __syncwarp();
       ++ec;
@@ -262,13 +294,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
   } else if (warp == kPtWarpMMA) {
     // ====================================================================== MMA issuer (rank 0, whole warp)
     if (rank == 0) {
-      const uint32_t idesc_qk = tc::make_idesc(1, 1, 128, kPage, false, false);
-      const uint32_t idesc_pv = tc::make_idesc(1, 1, 128, 256, false, true);
+      constexpr uint32_t idesc_qk = tc::make_idesc(1, 1, 128, kPage, false, false);
+      constexpr uint32_t idesc_pv = tc::make_idesc(1, 1, 128, 256, false, true);
       const uint16_t both = 3;
       const uint64_t q_desc = tc::desc_sw128(tc::smem_u32(sQ), 1024);
       const uint64_t p_desc = tc::desc_sw128(tc::smem_u32(sP), 1024);
       const uint64_t kv_desc = tc::desc_sw128(tc::smem_u32(sBuf), 1024);
       const uint64_t v_desc = tc::desc_sw128_lbo(tc::smem_u32(sBuf), kPtBlk, 1024);
+      const uint32_t tm_o = __shfl_sync(0xffffffffu, tmem + kPtTmemO, 0);
       uint32_t ec = 0, c = 0, v = 0;
       auto pv = [&](uint32_t cc, bool first) -> bool {
         const uint32_t b = cc % kPtNBuf, pb = cc & 1u;
@@ -277,12 +310,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         if (first && v > 0 && !tc::mbar_wait_cl_w(tc::smem_u32(&S->o_empty), (v - 1) & 1u, abort, status)) return false;
         tc::fence_after_sync();
         const uint64_t pa = p_desc + ((pb * kPtP) >> 4), vb = v_desc + ((b * kPtBuf) >> 4);
-        // K steps of 16 tokens: token half (4 blocks apart) x two steps of 16 rows
-        constexpr int kS = (16 * 128) >> 4, kH = (4 * kPtBlk) >> 4;
+        if (pt_elect()) {
+          // K steps of 16 tokens: token half (4 blocks apart) x two steps of 16 rows
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-          tc::mma_bf16_pair_x4_w<kS, kH, kH + kS>(tmem + kPtTmemO + 128 * p, pa, vb + ((2 * p * kPtBlk) >> 4), idesc_pv,
-                                                  first ? 0u : 1u);
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              pt_mma_pair(tm_o + 128 * p, pa + 2 * k, vb + ((2 * p * kPtBlk + (k >> 1) * 4 * kPtBlk + (k & 1) * 16 * 128) >> 4),
+                          idesc_pv, k > 0 || !first);
+        }
+        __syncwarp();
         tc::mma_commit_pair_w(tc::smem_u32(&S->buf_empty[b]), both);
         tc::mma_commit_pair_w(tc::smem_u32(&S->pv_done[pb]), both);
         return true;
@@ -290,14 +327,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       int4 e;
       bool prev_first = false;
       while (next_entry(ec, &e)) {
-        if (e.w & kPtEnd) break;
-        if (e.w & kPtEmpty) continue;
-        const bool first = e.w & kPtFirst, last = e.w & kPtLast;
+        const int info = __shfl_sync(0xffffffffu, e.w, 0);
+        if (info & kPtEnd) break;
+        if (info & kPtEmpty) continue;
+        const bool first = info & kPtFirst, last = info & kPtLast;
         const uint32_t b = c % kPtNBuf;
         if (first && !tc::mbar_wait_cl_w(tc::smem_u32(&S->q_full), v & 1u, abort, status)) break;
         if (!tc::mbar_wait_cl_w(tc::smem_u32(&S->buf_full[b]), (c / kPtNBuf) & 1u, abort, status)) break;
         tc::fence_after_sync();
-        tc::mma_qk36_pair_w<kPtBlk>(tmem + kPtTmemS + kPtHalf * (c & 1u), q_desc, kv_desc + ((b * kPtBuf) >> 4), idesc_qk);
+        const uint64_t kb = kv_desc + ((b * kPtBuf) >> 4);
+        const uint32_t d = tm_o + kPtTmemS - kPtTmemO + kPtHalf * (c & 1u);
+        if (pt_elect()) {
+#pragma unroll
+          for (int i = 0; i < 9; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              pt_mma_pair(d, q_desc + ((i * 8192) >> 4) + 2 * k, kb + ((i * kPtBlk) >> 4) + 2 * k, idesc_qk, i + k > 0);
+        }
+        __syncwarp();
         tc::mma_commit_pair_w(tc::smem_u32(&S->s_full[c & 1u]), both);
         if (last) tc::mma_commit_pair_w(tc::smem_u32(&S->q_empty), both);
         if (!first && !pv(c - 1, prev_first)) break;
@@ -315,12 +362,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
   } else {
     // ====================================================================== softmax + epilogue (warps 0-3)
     // The four warps leave the loop together (pt_any): they hold named barriers.
-    const int L = threadIdx.x;                     // TMEM lane
+    // Thread: TMEM lane L = (head h, token half) and 16 of that half's 32 tokens; the four threads of a head share its
+    // running maximum through shared memory.
+    const int L = threadIdx.x & 127, sub = threadIdx.x >> 7;
     const int h = L & 63, half = L >> 6;
     const int head = 64 * (int)rank + h;
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t p_full_r0 = tc::map_to_rank(tc::smem_u32(&S->p_full[0]), 0);
     const uint32_t o_empty_r0 = tc::map_to_rank(tc::smem_u32(&S->o_empty), 0);
+    const int tok0 = kPtHalf * half + 16 * sub;    // first token
+    const int ocol = 256 * half + 128 * sub;       // first value entry of the O columns that this thread rescales and stores
     __nv_bfloat16 *out = (__nv_bfloat16 *)a.o.out;
     float m_run = -INFINITY, l_run = 0.f;
     uint32_t ec = 0, c = 0;
@@ -331,13 +382,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       if (e.w & kPtEmpty) {                        // no page of the segment holds a token
         if (head < a.H) {
           if (part < 0) {
-            __nv_bfloat16 *o = out + ((int64_t)row * a.H + head) * kPtDv + 256 * half;
-            for (int i = 0; i < 256; i += 8) *reinterpret_cast<uint4 *>(o + i) = make_uint4(0, 0, 0, 0);
-            if (a.o.lse && half == 0) a.o.lse[(int64_t)row * a.H + head] = -INFINITY;
+            __nv_bfloat16 *o = out + ((int64_t)row * a.H + head) * kPtDv + ocol;
+            for (int i = 0; i < 128; i += 8) *reinterpret_cast<uint4 *>(o + i) = make_uint4(0, 0, 0, 0);
+            if (a.o.lse && ocol == 0) a.o.lse[(int64_t)row * a.H + head] = -INFINITY;
           } else {
-            float *o = a.o.part_o + ((int64_t)part * a.H + head) * kPtDv + 256 * half;
-            for (int i = 0; i < 256; i += 4) *reinterpret_cast<float4 *>(o + i) = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (half == 0) a.o.part_lse[(int64_t)part * a.H + head] = -INFINITY;
+            float *o = a.o.part_o + ((int64_t)part * a.H + head) * kPtDv + ocol;
+            for (int i = 0; i < 128; i += 4) *reinterpret_cast<float4 *>(o + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (ocol == 0) a.o.part_lse[(int64_t)part * a.H + head] = -INFINITY;
           }
         }
         continue;
@@ -347,25 +398,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         m_run = -INFINITY;
         l_run = 0.f;
       }
-      const int mine = e.y - kPtHalf * half;       // tokens of this thread's half
-      const bool have_s =
-          __all_sync(0xffffffffu, tc::mbar_wait_cl(tc::smem_u32(&S->s_full[c & 1u]), (c >> 1) & 1u, abort, status));
+      bool ok = tc::mbar_wait_cl_w(tc::smem_u32(&S->s_full[c & 1u]), (c >> 1) & 1u, abort, status);
       tc::fence_after_sync();
-      float sv[kPtHalf];
-      tc::tmem_ld32(tmem + lane_base + kPtTmemS + kPtHalf * (c & 1u), sv);
+      float sv[16];
+      pt_tmem_ld16(tmem + lane_base + kPtTmemS + kPtHalf * (c & 1u) + 16 * sub, sv);
       tc::tmem_wait_ld();
-      const int valid = have_s ? mine : 0;
+      const int valid = ok ? e.y - tok0 : 0;
       float mx = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kPtHalf; ++i) {
+      for (int i = 0; i < 16; ++i) {
         sv[i] = i < valid ? sv[i] * a.scale_log2 : -INFINITY;
         mx = fmaxf(mx, sv[i]);
       }
       const float mloc = fmaxf(m_run, mx);
-      S->xm[c & 1u][L] = mloc;
-      tc::named_bar_sync(2, 128);
-      const float m_new = fmaxf(mloc, S->xm[c & 1u][L ^ 64]);
-      bool pv_ok = true;
+      S->xm[c & 1u][threadIdx.x] = mloc;
+      tc::named_bar_sync(2, kPtSoftmax);
+      const float *xm = S->xm[c & 1u];
+      const float m_new = fmaxf(fmaxf(mloc, xm[threadIdx.x ^ 64]), fmaxf(xm[threadIdx.x ^ 128], xm[threadIdx.x ^ 192]));
       if (first) {
         m_run = m_new;
       } else {
@@ -374,17 +423,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         const bool want = m_new > m_run + kPtRescale;
         if (__any_sync(0xffffffffu, want)) {
           const uint32_t cp = c - 1;
-          pv_ok = __all_sync(0xffffffffu, tc::mbar_wait_cl(tc::smem_u32(&S->pv_done[cp & 1u]), (cp >> 1) & 1u, abort, status));
+          ok = tc::mbar_wait_cl_w(tc::smem_u32(&S->pv_done[cp & 1u]), (cp >> 1) & 1u, abort, status) && ok;
           tc::fence_after_sync();
           const float alpha = want ? tc::ex2(m_run - m_new) : 1.f;
-          if (pv_ok) {
-            for (int cc = 0; cc < 8; ++cc) {
+          if (ok) {
+            for (int cc = 0; cc < 4; ++cc) {
               float ov[32];
-              tc::tmem_ld32(tmem + lane_base + kPtTmemO + 32 * cc, ov);
+              tc::tmem_ld32(tmem + lane_base + kPtTmemO + 128 * sub + 32 * cc, ov);
               tc::tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) ov[i] *= alpha;
-              tc::tmem_st32(tmem + lane_base + kPtTmemO + 32 * cc, ov);
+              tc::tmem_st32(tmem + lane_base + kPtTmemO + 128 * sub + 32 * cc, ov);
             }
             tc::tmem_wait_st();
           }
@@ -395,29 +444,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         }
       }
       // this P buffer was last read by P V of page c - 2
-      if (c >= 2)
-        pv_ok = __all_sync(0xffffffffu, tc::mbar_wait_cl(tc::smem_u32(&S->pv_done[c & 1u]), ((c >> 1) & 1u) ^ 1u, abort, status)) &&
-                pv_ok;
+      if (c >= 2) ok = tc::mbar_wait_cl_w(tc::smem_u32(&S->pv_done[c & 1u]), ((c >> 1) & 1u) ^ 1u, abort, status) && ok;
       // P = exp2(z - m) in bf16 into the 128-byte-swizzled A operand; masked tokens hold -inf and give 0
-      if (pv_ok) {
+      if (ok) {
         const float m_use = m_run == -INFINITY ? 0.f : m_run;
         uint8_t *pbuf = sP + (c & 1u) * kPtP + h * 128;
-        float lsum = 0.f;
+        float ls[2] = {0.f, 0.f};
 #pragma unroll
-        for (int q8 = 0; q8 < kPtHalf / 8; ++q8) {
+        for (int q8 = 0; q8 < 2; ++q8) {
           uint32_t w4[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int t0 = 8 * q8 + 2 * i;
             const float p0 = tc::ex2(sv[t0] - m_use), p1 = tc::ex2(sv[t0 + 1] - m_use);
-            lsum += p0 + p1;
+            ls[q8] += p0 + p1;
             const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
             w4[i] = *reinterpret_cast<const uint32_t *>(&pb);
           }
-          const int kc = (kPtHalf / 8) * half + q8;
+          const int kc = tok0 / 8 + q8;
           *reinterpret_cast<uint4 *>(pbuf + ((kc ^ (h & 7)) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
-        l_run += lsum;
+        l_run += ls[0] + ls[1];
       }
       tc::fence_proxy_async();
       tc::fence_before_sync();
@@ -431,34 +478,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
 
       // ---- epilogue: wait for the last P V, normalise, store through a per-warp staging tile
       const uint32_t cl = c - 1;
-      const bool o_ok =
-          __all_sync(0xffffffffu, tc::mbar_wait_cl(tc::smem_u32(&S->pv_done[cl & 1u]), (cl >> 1) & 1u, abort, status));
+      ok = tc::mbar_wait_cl_w(tc::smem_u32(&S->pv_done[cl & 1u]), (cl >> 1) & 1u, abort, status) && ok;
       tc::fence_after_sync();
-      S->xl[L] = l_run;
-      tc::named_bar_sync(2, 128);
-      const float l_tot = l_run + S->xl[L ^ 64];
+      S->xl[threadIdx.x] = l_run;
+      tc::named_bar_sync(2, kPtSoftmax);
+      const float l_tot = (l_run + S->xl[threadIdx.x ^ 64]) + (S->xl[threadIdx.x ^ 128] + S->xl[threadIdx.x ^ 192]);
       const float inv = l_tot != 0.f ? 1.f / l_tot : 0.f;
-      if (o_ok) {
-        // both P buffers are free once the last P V finished: each warp stages a 32 x 32 fp32 tile (row = lane, 16-byte
-        // group j at j ^ (row & 7)) and writes whole 128-byte row segments
-        float *stg = reinterpret_cast<float *>(sP) + warp * 1024;
-        const int head0 = 64 * (int)rank + 32 * (warp & 1), col0 = 256 * (warp >> 1);
+      if (ok) {
+        // both P buffers are free once the last P V finished: each warp stages a 32 x 16 fp32 tile (row = lane, 16-byte
+        // group j at j ^ (row / 2 & 3)) and writes whole 64-byte row segments
+        float *stg = reinterpret_cast<float *>(sP) + warp * 512;
+        const int head0 = 64 * (int)rank + 32 * (warp & 1);
         if (head0 < a.H) {
           for (int cc = 0; cc < 8; ++cc) {
-            float ov[32];
-            tc::tmem_ld32(tmem + lane_base + kPtTmemO + 32 * cc, ov);
+            float ov[16];
+            pt_tmem_ld16(tmem + lane_base + kPtTmemO + 128 * sub + 16 * cc, ov);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<float4 *>(stg + lane * 32 + 4 * (j ^ (lane & 7))) =
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float4 *>(stg + lane * 16 + 4 * (j ^ ((lane >> 1) & 3))) =
                   make_float4(ov[4 * j] * inv, ov[4 * j + 1] * inv, ov[4 * j + 2] * inv, ov[4 * j + 3] * inv);
             __syncwarp();
             if (part < 0) {
 #pragma unroll
-              for (int it = 0; it < 4; ++it) {
-                const int r = 8 * it + (lane >> 2), j0 = 2 * (lane & 3);
-                const float4 f0 = *reinterpret_cast<const float4 *>(stg + r * 32 + 4 * (j0 ^ (r & 7)));
-                const float4 f1 = *reinterpret_cast<const float4 *>(stg + r * 32 + 4 * ((j0 + 1) ^ (r & 7)));
+              for (int it = 0; it < 2; ++it) {
+                const int r = 16 * it + (lane >> 1), j0 = 2 * (lane & 1), x = (r >> 1) & 3;
+                const float4 f0 = *reinterpret_cast<const float4 *>(stg + r * 16 + 4 * (j0 ^ x));
+                const float4 f1 = *reinterpret_cast<const float4 *>(stg + r * 16 + 4 * ((j0 + 1) ^ x));
                 const __nv_bfloat162 b0 = __floats2bfloat162_rn(f0.x, f0.y), b1 = __floats2bfloat162_rn(f0.z, f0.w);
                 const __nv_bfloat162 b2 = __floats2bfloat162_rn(f1.x, f1.y), b3 = __floats2bfloat162_rn(f1.z, f1.w);
                 uint4 w;
@@ -467,21 +513,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
                 w.z = *reinterpret_cast<const uint32_t *>(&b2);
                 w.w = *reinterpret_cast<const uint32_t *>(&b3);
                 if (head0 + r < a.H)
-                  *reinterpret_cast<uint4 *>(out + ((int64_t)row * a.H + head0 + r) * kPtDv + col0 + 32 * cc + 4 * j0) = w;
+                  *reinterpret_cast<uint4 *>(out + ((int64_t)row * a.H + head0 + r) * kPtDv + ocol + 16 * cc + 4 * j0) = w;
               }
             } else {
 #pragma unroll
-              for (int it = 0; it < 8; ++it) {
-                const int r = 4 * it + (lane >> 3), j = lane & 7;
+              for (int it = 0; it < 4; ++it) {
+                const int r = 8 * it + (lane >> 2), j = lane & 3;
                 if (head0 + r < a.H)
-                  *reinterpret_cast<float4 *>(a.o.part_o + ((int64_t)part * a.H + head0 + r) * kPtDv + col0 + 32 * cc + 4 * j) =
-                      *reinterpret_cast<const float4 *>(stg + r * 32 + 4 * (j ^ (r & 7)));
+                  *reinterpret_cast<float4 *>(a.o.part_o + ((int64_t)part * a.H + head0 + r) * kPtDv + ocol + 16 * cc + 4 * j) =
+                      *reinterpret_cast<const float4 *>(stg + r * 16 + 4 * (j ^ ((r >> 1) & 3)));
               }
             }
             __syncwarp();
           }
         }
-        if (half == 0 && head < a.H) {
+        if (ocol == 0 && head < a.H) {
           const float lse = l_tot != 0.f ? (m_run + __log2f(l_tot)) * 0.69314718055994531f : -INFINITY;
           if (part >= 0) a.o.part_lse[(int64_t)part * a.H + head] = lse;
           else if (a.o.lse) a.o.lse[(int64_t)row * a.H + head] = lse;
@@ -535,7 +581,7 @@ static bool pt_map(CUtensorMap *m, const void *base, uint32_t rank, uint64_t d1,
 // The main kernel of the latent cache; returns the workers (CTA pairs) through *workers for the join.
 dsa_status_t paged_mla_launch(const void *q, const void *kv, int H, float softmax_scale, const PagedView &view,
                               const PagedOut &o, int max_workers, cudaStream_t stream, int num_sms, int *workers) {
-  PtArgs a{view, o, H, softmax_scale * 1.4426950408889634f, 2};
+  PtArgs a{view, o, (const __nv_bfloat16 *)kv, H, softmax_scale * 1.4426950408889634f, 2};
   CUtensorMap tm_q, tm_tiles, tm_rows;
   const uint64_t rows = (uint64_t)view.num_blocks * kPage;
   if (!pt_map(&tm_q, q, 3, (uint64_t)H, (uint64_t)view.T, 64) || !pt_map(&tm_tiles, kv, 2, rows, 1, kPtHalf) ||

@@ -506,6 +506,24 @@ def test_page_lists(heads, f32, kb):
     c.check(q, 0.07, out, lse, pages)
 
 
+@pytest.mark.parametrize("heads,f32", [(128, None), (4, (64, 64))])
+def test_long_runs_of_rows_whose_lists_hold_nothing(heads, f32):
+    """Far more rows without a page than pages that a worker has in flight, between rows with one to five pages."""
+    rng = np.random.default_rng(0)
+    lens = [min(100 + 7 * i, 400) for i in range(2000)]
+    pages = np.full((2000, 6), -1)
+    for b in (0, 3, 40, 41, 42, 43, 700, 1400, 1999):
+        have = -(-lens[b] // 64)
+        n = min(have, int(rng.integers(1, 6)))
+        pages[b, rng.permutation(6)[:n]] = rng.permutation(have)[:n]
+    pages[5:30] = 1 << 20                                               # past every sequence
+    c = _Cache(lens, f32=f32, seed=1)
+    q = c.q(heads)
+    out, lse = c.attend(q, 0.07, pages=_i32(pages))
+    B.dsa_read_device_status(c.ws)
+    c.check(q, 0.07, out, lse, pages)
+
+
 @pytest.mark.parametrize("heads,f32", [(128, None), (32, None), (8, (64, 64))])
 def test_one_long_row_and_many_short_ones(heads, f32):
     for lens in ([40001], [33] * 300, [1] * 200 + [30000] + [70] * 100, [0] * 7):
