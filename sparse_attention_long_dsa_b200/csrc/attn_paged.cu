@@ -161,29 +161,91 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a, 
 
 // ------------------------------------------------------------------------------------------------ join
 // out[row, h, :] = sum_w exp(lse_w - lse) o_w,  lse = log sum_w exp(lse_w)  over the workers w that hold a part of the row.
-// One CTA per (worker in which a split row ends, head).
+// One CTA per (split row, head); at most min(T, workers) rows are split, and CTA x finds the x-th of them in info.  Four
+// groups of 128 threads take every fourth part each, four loads in flight per thread, and add up in a fixed order: a row
+// over 74 workers is five rounds of loads instead of 74.
+constexpr int kPcGroups = 4, kPcThreads = 128 * kPcGroups, kPcMaxParts = 160;
+
 template <typename T>
-__global__ void __launch_bounds__(128) paged_combine_kernel(const PagedOut o, int H, int Dv) {
+__global__ void __launch_bounds__(kPcThreads) paged_combine_kernel(const PagedOut o, int workers, int H, int Dv) {
+  __shared__ float s_w[kPcMaxParts];
+  __shared__ float s_acc[kPcGroups - 1][512];
+  __shared__ int s_last, s_first, s_row;
   pdl_wait();
   pdl_trigger();
-  const int last = blockIdx.x, h = blockIdx.y;
-  const int2 who = __ldg(o.info + last);
-  if (who.x < 0) return;
-  const int n = last - who.y + 1;
+  const int h = blockIdx.y, tid = threadIdx.x;
+  if (tid < 32) {
+    int seen = 0, last = -1;
+    int2 who = make_int2(-1, 0);
+    for (int w0 = 0; w0 < workers; w0 += 32) {
+      const int2 i = w0 + tid < workers ? __ldg(o.info + w0 + tid) : make_int2(-1, 0);
+      const uint32_t m = __ballot_sync(0xffffffffu, i.x >= 0);
+      const int nth = seen + __popc(m & ((1u << tid) - 1u));
+      const uint32_t me = __ballot_sync(0xffffffffu, i.x >= 0 && nth == (int)blockIdx.x);
+      if (me) {
+        const int l = __ffs(me) - 1;
+        last = w0 + l;
+        who.x = __shfl_sync(0xffffffffu, i.x, l);
+        who.y = __shfl_sync(0xffffffffu, i.y, l);
+        break;
+      }
+      seen += __popc(m);
+    }
+    if (tid == 0) {
+      s_last = last;
+      s_first = who.y;
+      s_row = who.x;
+    }
+  }
+  __syncthreads();
+  const int row = s_row, first = s_first;
+  if (row < 0) return;
+  const int n = s_last - first + 1;
   // part s: the first worker's odd slot, then the even slots of the workers after it
-  auto slot = [&](int s) { return (int64_t)(2 * (who.y + s) + (s == 0 ? 1 : 0)) * H + h; };
+  auto slot = [&](int s) { return (int64_t)(2 * (first + s) + (s == 0 ? 1 : 0)) * H + h; };
+  for (int s = tid; s < n; s += kPcThreads) s_w[s] = __ldg(o.part_lse + slot(s));
+  __syncthreads();
   float mx = -INFINITY;
-  for (int s = 0; s < n; ++s) mx = fmaxf(mx, __ldg(o.part_lse + slot(s)));
+  for (int s = 0; s < n; ++s) mx = fmaxf(mx, s_w[s]);
   float tot = 0.f;
   if (mx != -INFINITY)
-    for (int s = 0; s < n; ++s) tot += expf(__ldg(o.part_lse + slot(s)) - mx);
-  for (int d = threadIdx.x; d < Dv; d += 128) {
-    float acc = 0.f;
-    if (tot > 0.f)
-      for (int s = 0; s < n; ++s) acc = fmaf(expf(__ldg(o.part_lse + slot(s)) - mx) / tot, __ldg(o.part_o + slot(s) * Dv + d), acc);
-    ps_store((T *)o.out + ((int64_t)who.x * H + h) * Dv + d, acc);
+    for (int s = 0; s < n; ++s) tot += expf(s_w[s] - mx);
+  const float inv = tot != 0.f ? 1.f / tot : 0.f;
+  const int g = tid >> 7, t = tid & 127;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  if (tot != 0.f) {
+    if ((Dv & 3) == 0) {
+      if (4 * t < Dv)
+#pragma unroll 4
+        for (int s = g; s < n; s += kPcGroups) {
+          const float4 v = __ldg(reinterpret_cast<const float4 *>(o.part_o + slot(s) * Dv) + t);
+          const float w = expf(s_w[s] - mx) * inv;
+          acc[0] = fmaf(w, v.x, acc[0]);
+          acc[1] = fmaf(w, v.y, acc[1]);
+          acc[2] = fmaf(w, v.z, acc[2]);
+          acc[3] = fmaf(w, v.w, acc[3]);
+        }
+    } else {
+#pragma unroll 4
+      for (int s = g; s < n; s += kPcGroups) {
+        const float w = expf(s_w[s] - mx) * inv;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (4 * t + i < Dv) acc[i] = fmaf(w, __ldg(o.part_o + slot(s) * Dv + 4 * t + i), acc[i]);
+      }
+    }
   }
-  if (o.lse && threadIdx.x == 0) o.lse[(int64_t)who.x * H + h] = tot > 0.f ? mx + logf(tot) : -INFINITY;
+  if (g > 0)
+    for (int i = 0; i < 4; ++i) s_acc[g - 1][4 * t + i] = acc[i];
+  __syncthreads();
+  if (g == 0) {
+    T *out = (T *)o.out + ((int64_t)row * H + h) * Dv;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (4 * t + i < Dv) ps_store(out + 4 * t + i, (acc[i] + s_acc[0][4 * t + i]) + (s_acc[1][4 * t + i] + s_acc[2][4 * t + i]));
+    }
+    if (o.lse && t == 0) o.lse[(int64_t)row * H + h] = tot != 0.f ? mx + logf(tot) : -INFINITY;
+  }
 }
 
 // ------------------------------------------------------------------------------------------------ host
@@ -231,8 +293,8 @@ dsa_status_t paged_attn_launch(const void *q, bool bf16, const void *kv, const v
     int workers = 0;
     const dsa_status_t st = paged_mla_launch(q, kv, H, scale, a.view, a.o, paged_max_workers(Dv), stream, num_sms, &workers);
     if (st != DSA_OK) return st;
-    DSA_LAUNCH_PDL("paged_combine_kernel", paged_combine_kernel<__nv_bfloat16>, dim3(workers, H), dim3(128), 0, stream, a.o, H,
-                   Dv);
+    DSA_LAUNCH_PDL("paged_combine_kernel", paged_combine_kernel<__nv_bfloat16>, dim3(std::min(workers, b->total_q), H),
+                   dim3(kPcThreads), 0, stream, a.o, workers, H, Dv);
     return DSA_OK;
   }
   const int workers = std::min(num_sms, paged_max_workers(Dv));
@@ -240,7 +302,8 @@ dsa_status_t paged_attn_launch(const void *q, bool bf16, const void *kv, const v
   const size_t smem = 4 * ((size_t)kPsHeads * 4 * D4 + (size_t)kPsTok * ps_stride(Dqk) + kPsHeads * kPsTok + (size_t)kPsTok * Dv);
   cudaFuncSetAttribute(paged_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   DSA_LAUNCH_PDL("paged_simt_kernel", paged_simt_kernel, dim3(workers), dim3(kPsThreads), smem, stream, a, 2);
-  DSA_LAUNCH_PDL("paged_combine_kernel", paged_combine_kernel<float>, dim3(workers, H), dim3(128), 0, stream, a.o, H, Dv);
+  DSA_LAUNCH_PDL("paged_combine_kernel", paged_combine_kernel<float>, dim3(std::min(workers, b->total_q), H),
+                 dim3(kPcThreads), 0, stream, a.o, workers, H, Dv);
   return DSA_OK;
 }
 

@@ -31,15 +31,16 @@ namespace dsa {
 
 constexpr int kPtD = 576, kPtDv = 512;
 constexpr int kPtHalf = kPage / 2;
-constexpr int kPtNBuf = 3;
+constexpr int kPtNBuf = 4;                         // page buffers
+constexpr int kPtNS = 3;                           // score tiles: QK^T runs kPtNS - 1 pages ahead of P V
 constexpr int kPtRing = 8;                         // published pages in flight
 constexpr int kPtThreads = 384;                    // softmax x 8, keys, MMA, resolve, values
-constexpr int kPtSoftmax = 256;
+constexpr int kPtGroup = 128;                      // threads of a softmax group (4 warps)
 constexpr int kPtWarpKeys = 8, kPtWarpMMA = 9, kPtWarpResolve = 10, kPtWarpValues = 11;
 constexpr uint32_t kPtBlk = kPtHalf * 128;         // one 64-entry block of a CTA's 32 tokens: 4 KB
 constexpr uint32_t kPtBuf = 9 * kPtBlk;
 constexpr uint32_t kPtQ = 9 * 8192;
-constexpr uint32_t kPtP = 8192;                    // [64 heads][64 tokens] bf16
+constexpr uint32_t kPtP = 8192;                    // [64 heads][64 tokens] bf16; epilogue staging
 constexpr uint32_t kPtTmemO = 0, kPtTmemS = 256;
 constexpr float kPtRescale = 8.0f;
 constexpr int kPtFirst = 1, kPtLast = 2, kPtEmpty = 4, kPtEnd = 8;
@@ -49,14 +50,20 @@ struct PtSmem {
   uint64_t buf_empty[kPtNBuf];      // MMA commit to both CTAs after P V
   uint64_t v_full[kPtNBuf];         // rank 0: bytes of both CTAs' peer values
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[kPtNS];
+  uint64_t p_full;
+  uint64_t pv_done[2];              // by page parity: a group waits for every phase of the other group's barrier
   uint64_t o_empty, drain;
   uint64_t ent_full[kPtRing], ent_empty[kPtRing];
   uint32_t tmem_base;
   int abort;
   int4 ent[kPtRing];                // physical row, tokens, row, flags | (part + 1) << 8
-  float xm[2][kPtSoftmax];
-  float xl[kPtSoftmax];
+  uint64_t dec[2];                  // the references of a page are decided, by its parity
+  uint64_t l_ready[2];              // lp is written
+  uint64_t st_free;                 // the staging tiles of a segment's epilogue have been read
+  float ref[64];                    // reference of each head, log2 units
+  float x[2][kPtGroup];             // maxima, then sums, of the threads of a head
+  float lp[2][kPtGroup];            // the other group's sums of a segment, by its parity
   uint32_t tmp[33];
   PagedPlan plan;
 };
@@ -70,6 +77,28 @@ struct PtArgs {
   int min_slots;
 };
 
+// Waits of whole warps.  A phase that is already complete costs one test and a branch (about 40 cycles; the general form with
+// its loop and warp vote inline took 200, and there are ten of them on the way of a page).  false: the wait ran out.
+__device__ __noinline__ bool pt_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *status) {
+  return tc::mbar_wait(bar, parity, abort, status);
+}
+__device__ __noinline__ bool pt_wait_slow_cl(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *status) {
+  return tc::mbar_wait_cl(bar, parity, abort, status);
+}
+__device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *status) {
+  bool ok = tc::mbar_try_wait(bar, parity);
+  if (__builtin_expect(!ok, 0)) ok = pt_wait_slow(bar, parity, abort, status);
+  __syncwarp();
+  return ok;
+}
+// for barriers that receive the other CTA's arrivals
+__device__ __forceinline__ bool pt_wait_cl(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *status) {
+  bool ok = tc::mbar_try_wait_cl(bar, parity);
+  if (__builtin_expect(!ok, 0)) ok = pt_wait_slow_cl(bar, parity, abort, status);
+  __syncwarp();
+  return ok;
+}
+// .cta_group::2: the completion bytes may be counted on the other CTA's barrier
 __device__ __forceinline__ void pt_load_3d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
@@ -77,20 +106,19 @@ __device__ __forceinline__ void pt_load_3d_pair(uint32_t dst, const CUtensorMap 
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-// true if any of the softmax threads says so
-__device__ __forceinline__ bool pt_any(bool x) {
+// true if any thread of softmax group g says so
+__device__ __forceinline__ bool pt_any(int g, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 3, %2, p;\n\t"
+      "barrier.cta.red.or.pred q, %3, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x), "n"(kPtSoftmax)
+      : "r"((uint32_t)x), "n"(kPtGroup), "r"(3 + g)
       : "memory");
   return r != 0;
 }
-
 __device__ __forceinline__ bool pt_elect() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
@@ -119,11 +147,12 @@ __device__ __forceinline__ void pt_tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 32 tokens of a page, from token t0 on, `n` 64-entry blocks: column block src + i to dst + i * 4 KB.  Whole warp.
-__device__ __forceinline__ void pt_copy(const CUtensorMap *tiles, const CUtensorMap *rows, int lane, int phys, int ntok, int t0,
+// 32 tokens of a page, from token t0 on: the map's 64-entry blocks from `src` on (`n` of them) to consecutive 4 KB at dst.
+// Whole warp.
+__device__ __forceinline__ void pt_copy(const CUtensorMap *blocks, const CUtensorMap *rows, int lane, int phys, int ntok, int t0,
                                         int oob, int src, int n, uint32_t dst, uint32_t bar) {
   if (ntok == kPage) {
-    if (lane < n) tc::tma_load_2d_pair(dst + lane * kPtBlk, tiles, (src + lane) * 64, phys + t0, bar);
+    if (lane == 0) pt_load_3d_pair(dst, blocks, 0, phys + t0, src, bar);
   } else if (lane < kPtHalf / 4) {
     int r4[4];
 #pragma unroll
@@ -136,15 +165,19 @@ __device__ __forceinline__ void pt_copy(const CUtensorMap *tiles, const CUtensor
   }
 }
 
+struct PtMaps {
+  CUtensorMap q;                    // [T][H][576] in boxes of 64 heads x 64 entries
+  CUtensorMap keys, values;         // [9 blocks][tokens][64] in boxes of 32 tokens and 9 / 4 blocks
+  CUtensorMap row;                  // [tokens][576] in boxes of one token x 64 entries (gather4)
+};
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
-    paged_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_tiles,
-                     const __grid_constant__ CUtensorMap tm_rows, const PtArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    paged_mla_kernel(const __grid_constant__ PtMaps tm, const PtArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sQ = smem;                              // [9 blocks][64 heads][128 B]
-  uint8_t *sBuf = sQ + kPtQ;                       // 3 x [9 blocks][32 tokens][128 B]
-  uint8_t *sP = sBuf + kPtNBuf * kPtBuf;           // 2 x P; epilogue staging
-  PtSmem *S = (PtSmem *)(sP + 2 * kPtP);
+  uint8_t *sBuf = sQ + kPtQ;                       // 4 x [9 blocks][32 tokens][128 B]
+  uint8_t *sP = sBuf + kPtNBuf * kPtBuf;
+  PtSmem *S = (PtSmem *)(sP + kPtP);
 
   const uint32_t rank = tc::cluster_ctarank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -156,24 +189,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       tc::mbar_init(tc::smem_u32(&S->buf_empty[i]), 1);
       tc::mbar_init(tc::smem_u32(&S->v_full[i]), 1);
     }
+    for (int i = 0; i < kPtNS; ++i) tc::mbar_init(tc::smem_u32(&S->s_full[i]), 1);
+    tc::mbar_init(tc::smem_u32(&S->p_full), 8);
+    tc::mbar_init(tc::smem_u32(&S->st_free), 4);
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(tc::smem_u32(&S->s_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&S->p_full[i]), 2 * kPtSoftmax / 32);
       tc::mbar_init(tc::smem_u32(&S->pv_done[i]), 1);
+      tc::mbar_init(tc::smem_u32(&S->dec[i]), 4);
+      tc::mbar_init(tc::smem_u32(&S->l_ready[i]), 4);
     }
     tc::mbar_init(tc::smem_u32(&S->q_full), 1);
     tc::mbar_init(tc::smem_u32(&S->q_empty), 1);
-    tc::mbar_init(tc::smem_u32(&S->o_empty), 2 * kPtSoftmax / 32);
+    tc::mbar_init(tc::smem_u32(&S->o_empty), 8);
     tc::mbar_init(tc::smem_u32(&S->drain), 1);
     for (int i = 0; i < kPtRing; ++i) {
       tc::mbar_init(tc::smem_u32(&S->ent_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&S->ent_empty[i]), kPtSoftmax / 32 + (rank == 0 ? 3 : 2));   // keys, values, MMA (rank 0)
+      tc::mbar_init(tc::smem_u32(&S->ent_empty[i]), rank == 0 ? 11 : 10);   // softmax x 8, keys, values, MMA (rank 0)
     }
     S->abort = 0;
     tc::fence_barrier_init();
-    tc::prefetch_tmap(&tm_q);
-    tc::prefetch_tmap(&tm_tiles);
-    tc::prefetch_tmap(&tm_rows);
+    tc::prefetch_tmap(&tm.q);
+    tc::prefetch_tmap(&tm.keys);
+    tc::prefetch_tmap(&tm.values);
+    tc::prefetch_tmap(&tm.row);
   }
   if (warp == kPtWarpMMA) {
     tc::tmem_alloc2(tc::smem_u32(&S->tmem_base), 512);
@@ -194,7 +231,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
   // next entry of the ring, for a whole warp: false ends the role (the end of the work, or a wait that ran out)
   auto next_entry = [&](uint32_t &ec, int4 *e) -> bool {
     const uint32_t slot = ec % kPtRing;
-    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&S->ent_full[slot]), (ec / kPtRing) & 1u, abort, status));
+    const bool ok = pt_wait(tc::smem_u32(&S->ent_full[slot]), (ec / kPtRing) & 1u, abort, status);
     if (!ok) return false;
     *e = S->ent[slot];
     __syncwarp();
@@ -209,8 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     uint32_t ec = 0;
     auto push = [&](int phys, int ntok, int row, int info) {
       const uint32_t slot = ec % kPtRing;
-      const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&S->ent_empty[slot]), ((ec / kPtRing) & 1u) ^ 1u, abort,
-                                                            status));
+      const bool ok = pt_wait(tc::smem_u32(&S->ent_empty[slot]), ((ec / kPtRing) & 1u) ^ 1u, abort, status);
       if (lane == 0 && ok) {
         S->ent[slot] = make_int4(phys, ntok, row, info);
         tc::mbar_arrive(tc::smem_u32(&S->ent_full[slot]));
@@ -257,17 +293,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       if (e.w & kPtEnd) break;
       if (e.w & kPtEmpty) continue;
       const uint32_t b = c % kPtNBuf;
-      if (!tc::mbar_wait_cl_w(tc::smem_u32(&S->buf_empty[b]), ((c / kPtNBuf) & 1u) ^ 1u, abort, status)) break;
+      if (!pt_wait(tc::smem_u32(&S->buf_empty[b]), ((c / kPtNBuf) & 1u) ^ 1u, abort, status)) break;
       if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->buf_full[b]), 2u * kPtBuf);
       __syncwarp();
-      pt_copy(&tm_tiles, &tm_rows, lane, e.x, e.y, kPtHalf * (int)rank, oob, 0, 9, tc::smem_u32(sBuf + b * kPtBuf),
+      pt_copy(&tm.keys, &tm.row, lane, e.x, e.y, kPtHalf * (int)rank, oob, 0, 9, tc::smem_u32(sBuf + b * kPtBuf),
               buf_full_r0 + b * 8);
       if (e.w & kPtFirst) {
         // q is overwritten once the previous segment's last QK^T has run
-        if (v > 0 && !tc::mbar_wait_cl_w(tc::smem_u32(&S->q_empty), (v - 1) & 1u, abort, status)) break;
+        if (v > 0 && !pt_wait(tc::smem_u32(&S->q_empty), (v - 1) & 1u, abort, status)) break;
         if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->q_full), 2u * kPtQ);
         __syncwarp();
-        if (lane < 9) pt_load_3d_pair(tc::smem_u32(sQ + lane * 8192), &tm_q, lane * 64, 64 * (int)rank, e.z, q_full_r0);
+        if (lane < 9) pt_load_3d_pair(tc::smem_u32(sQ + lane * 8192), &tm.q, lane * 64, 64 * (int)rank, e.z, q_full_r0);
         ++v;
       }
       ++c;
@@ -284,10 +320,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       if (e.w & kPtEmpty) continue;
       const uint32_t b = c % kPtNBuf;
       // QK^T of this page has read the buffers
-      if (!tc::mbar_wait_cl_w(tc::smem_u32(&S->s_full[c & 1u]), (c >> 1) & 1u, abort, status)) break;
+      if (!pt_wait(tc::smem_u32(&S->s_full[c % kPtNS]), (c / kPtNS) & 1u, abort, status)) break;
       if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->v_full[b]), 2u * 4u * kPtBlk);
       __syncwarp();
-      pt_copy(&tm_tiles, &tm_rows, lane, e.x, e.y, kPtHalf * (int)(rank ^ 1u), oob, src, 4,
+      pt_copy(&tm.values, &tm.row, lane, e.x, e.y, kPtHalf * (int)(rank ^ 1u), oob, src, 4,
               tc::smem_u32(sBuf + b * kPtBuf + dst * kPtBlk), v_full_r0 + b * 8);
       ++c;
     }
@@ -302,41 +338,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       const uint64_t kv_desc = tc::desc_sw128(tc::smem_u32(sBuf), 1024);
       const uint64_t v_desc = tc::desc_sw128_lbo(tc::smem_u32(sBuf), kPtBlk, 1024);
       const uint32_t tm_o = __shfl_sync(0xffffffffu, tmem + kPtTmemO, 0);
-      uint32_t ec = 0, c = 0, v = 0;
-      auto pv = [&](uint32_t cc, bool first) -> bool {
-        const uint32_t b = cc % kPtNBuf, pb = cc & 1u;
-        if (!tc::mbar_wait_cl_w(tc::smem_u32(&S->p_full[pb]), (cc >> 1) & 1u, abort, status)) return false;
-        if (!tc::mbar_wait_cl_w(tc::smem_u32(&S->v_full[b]), (cc / kPtNBuf) & 1u, abort, status)) return false;
-        if (first && v > 0 && !tc::mbar_wait_cl_w(tc::smem_u32(&S->o_empty), (v - 1) & 1u, abort, status)) return false;
+      uint32_t ec = 0, c = 0, done = 0, segs = 0, segs_pv = 0;      // pages with QK^T, with P V; segments begun
+      uint32_t firsts = 0;                                          // bit i: page c - 1 - i begins a segment
+      auto pv = [&]() -> bool {                                     // P V of page `done`
+        const bool first = (firsts >> (c - done - 1)) & 1u;
+        const uint32_t b = done % kPtNBuf;
+        if (!pt_wait_cl(tc::smem_u32(&S->p_full), done & 1u, abort, status)) return false;
+        if (!pt_wait(tc::smem_u32(&S->v_full[b]), (done / kPtNBuf) & 1u, abort, status)) return false;
+        if (first) {
+          if (segs_pv > 0 && !pt_wait_cl(tc::smem_u32(&S->o_empty), (segs_pv - 1) & 1u, abort, status)) return false;
+          ++segs_pv;
+        }
         tc::fence_after_sync();
-        const uint64_t pa = p_desc + ((pb * kPtP) >> 4), vb = v_desc + ((b * kPtBuf) >> 4);
+        const uint64_t vb = v_desc + ((b * kPtBuf) >> 4);
         if (pt_elect()) {
           // K steps of 16 tokens: token half (4 blocks apart) x two steps of 16 rows
 #pragma unroll
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              pt_mma_pair(tm_o + 128 * p, pa + 2 * k, vb + ((2 * p * kPtBlk + (k >> 1) * 4 * kPtBlk + (k & 1) * 16 * 128) >> 4),
-                          idesc_pv, k > 0 || !first);
+              pt_mma_pair(tm_o + 128 * p, p_desc + 2 * k,
+                          vb + ((2 * p * kPtBlk + (k >> 1) * 4 * kPtBlk + (k & 1) * 16 * 128) >> 4), idesc_pv, k > 0 || !first);
         }
         __syncwarp();
         tc::mma_commit_pair_w(tc::smem_u32(&S->buf_empty[b]), both);
-        tc::mma_commit_pair_w(tc::smem_u32(&S->pv_done[pb]), both);
+        tc::mma_commit_pair_w(tc::smem_u32(&S->pv_done[done & 1u]), both);
+        ++done;
         return true;
       };
       int4 e;
-      bool prev_first = false;
-      while (next_entry(ec, &e)) {
+      bool ok = true;
+      while (ok && (ok = next_entry(ec, &e))) {
         const int info = __shfl_sync(0xffffffffu, e.w, 0);
         if (info & kPtEnd) break;
-        if (info & kPtEmpty) continue;
-        const bool first = info & kPtFirst, last = info & kPtLast;
+        if (info & kPtEmpty) {
+          // A run of these may fill the ring before the next page, and the softmax frees it only after the P V it waits for.
+          while (ok && done < c) ok = pv();
+          continue;
+        }
         const uint32_t b = c % kPtNBuf;
-        if (first && !tc::mbar_wait_cl_w(tc::smem_u32(&S->q_full), v & 1u, abort, status)) break;
-        if (!tc::mbar_wait_cl_w(tc::smem_u32(&S->buf_full[b]), (c / kPtNBuf) & 1u, abort, status)) break;
+        if (info & kPtFirst) ok = pt_wait(tc::smem_u32(&S->q_full), segs++ & 1u, abort, status);
+        if (ok) ok = pt_wait(tc::smem_u32(&S->buf_full[b]), (c / kPtNBuf) & 1u, abort, status);
+        if (!ok) break;
         tc::fence_after_sync();
+        // score tile c % kPtNS: read before P V of page c - kPtNS was issued
         const uint64_t kb = kv_desc + ((b * kPtBuf) >> 4);
-        const uint32_t d = tm_o + kPtTmemS - kPtTmemO + kPtHalf * (c & 1u);
+        const uint32_t d = tm_o + kPtTmemS - kPtTmemO + kPtHalf * (c % kPtNS);
         if (pt_elect()) {
 #pragma unroll
           for (int i = 0; i < 9; ++i)
@@ -345,189 +392,212 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
               pt_mma_pair(d, q_desc + ((i * 8192) >> 4) + 2 * k, kb + ((i * kPtBlk) >> 4) + 2 * k, idesc_qk, i + k > 0);
         }
         __syncwarp();
-        tc::mma_commit_pair_w(tc::smem_u32(&S->s_full[c & 1u]), both);
-        if (last) tc::mma_commit_pair_w(tc::smem_u32(&S->q_empty), both);
-        if (!first && !pv(c - 1, prev_first)) break;
-        prev_first = first;
-        if (last) {
-          if (!pv(c, first)) break;
-          ++v;
-        }
+        tc::mma_commit_pair_w(tc::smem_u32(&S->s_full[c % kPtNS]), both);
+        if (info & kPtLast) tc::mma_commit_pair_w(tc::smem_u32(&S->q_empty), both);
+        firsts = firsts << 1 | (uint32_t)(info & kPtFirst);
         ++c;
+        if (c - done == kPtNS) ok = pv();
       }
+      while (ok && done < c) ok = pv();
       tc::mma_commit_pair_local_w(tc::smem_u32(&S->drain));
       volatile int no_abort = 0;
       __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&S->drain), 0, &no_abort, status));
     }
   } else {
-    // ====================================================================== softmax + epilogue (warps 0-3)
-    // The four warps leave the loop together (pt_any): they hold named barriers.
-    // Thread: TMEM lane L = (head h, token half) and 16 of that half's 32 tokens; the four threads of a head share its
-    // running maximum through shared memory.
-    const int L = threadIdx.x & 127, sub = threadIdx.x >> 7;
+    // ====================================================================== softmax + epilogue (two groups of 4 warps)
+    // Group g takes the pages c with c % 2 == g.  Thread: TMEM lane L = (head h, token half), that half's 32 tokens.  P of a
+    // page is 2^(z - ref) with one reference per head for both groups: the owner of page c decides it after the owner of
+    // page c - 1 has (dec), changes it only where a score outgrows it by 2^8, and then rescales O (exact: the final division
+    // uses the same reference).  The warps of a group leave the loop together (one vote per entry): they hold named barriers.
+    const int g = warp >> 2, L = threadIdx.x & (kPtGroup - 1);
     const int h = L & 63, half = L >> 6;
     const int head = 64 * (int)rank + h;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t p_full_r0 = tc::map_to_rank(tc::smem_u32(&S->p_full[0]), 0);
+    const uint32_t p_full_r0 = tc::map_to_rank(tc::smem_u32(&S->p_full), 0);
     const uint32_t o_empty_r0 = tc::map_to_rank(tc::smem_u32(&S->o_empty), 0);
-    const int tok0 = kPtHalf * half + 16 * sub;    // first token
-    const int ocol = 256 * half + 128 * sub;       // first value entry of the O columns that this thread rescales and stores
     __nv_bfloat16 *out = (__nv_bfloat16 *)a.o.out;
-    float m_run = -INFINITY, l_run = 0.f;
-    uint32_t ec = 0, c = 0;
-    int4 e;
+    float m_run = -INFINITY, l_run = 0.f;          // this thread's tokens of the segment: reference, sum of weights
+    uint32_t ec = 0, c = 0, seg = 0;
+    int4 e = make_int4(0, 0, 0, 0);
     for (;;) {
-      if (pt_any(!next_entry(ec, &e)) || (e.w & kPtEnd)) break;
+      bool ok = next_entry(ec, &e);
+      const bool page = ok && !(e.w & (kPtEnd | kPtEmpty));
+      const bool first = e.w & kPtFirst, last = e.w & kPtLast;
+      if (page && first) {
+        m_run = -INFINITY;
+        l_run = 0.f;
+      }
+      if (page && (int)(c & 1u) != g) {            // the other group's page
+        if (last) {                                // hand over the sums, at the segment's final references
+          pt_wait(tc::smem_u32(&S->dec[c & 1u]), (c >> 1) & 1u, abort, status);
+          S->lp[seg & 1u][L] = l_run != 0.f ? l_run * tc::ex2(m_run - S->ref[h]) : 0.f;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(tc::smem_u32(&S->l_ready[seg & 1u]));
+          ++seg;
+        }
+        ++c;
+        continue;
+      }
+      float sv[kPtHalf];
+      float mx = -INFINITY;
+      if (page) {
+        ok = pt_wait(tc::smem_u32(&S->s_full[c % kPtNS]), (c / kPtNS) & 1u, abort, status);
+        tc::fence_after_sync();
+        tc::tmem_ld32(tmem + lane_base + kPtTmemS + kPtHalf * (c % kPtNS), sv);
+        tc::tmem_wait_ld();
+        if (e.y < kPage) {
+#pragma unroll
+          for (int i = 0; i < kPtHalf; ++i) sv[i] = i < e.y - kPtHalf * half ? sv[i] : -INFINITY;
+        }
+        float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+        for (int i = 4; i < kPtHalf; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
+        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+        if (c > 0) ok = pt_wait(tc::smem_u32(&S->dec[(c - 1) & 1u]), ((c - 1) >> 1) & 1u, abort, status) && ok;
+        if (!first) {
+          const float r = S->ref[h];
+          if (r != m_run) {                        // the other group has moved it
+            l_run *= tc::ex2(m_run - r);
+            m_run = r;
+          }
+        }
+      }
+      // One vote per entry: has a wait run out, or a score outgrown its reference?
+      if (pt_any(g, !ok || (page && (first || mx > m_run + kPtRescale)))) {
+        if (pt_any(g, !ok)) break;
+        // the new reference of a head is the largest score so far
+        S->x[g][L] = fmaxf(m_run, mx);
+        tc::named_bar_sync(1 + g, kPtGroup);
+        const float m_new = fmaxf(S->x[g][L], S->x[g][L ^ 64]);
+        // TMEM accesses are warp-collective: every row of the warp is brought to its new reference.  P V of the previous
+        // page must have finished before O is touched.
+        if (!first && __any_sync(0xffffffffu, m_new > m_run)) {
+          ok = pt_wait(tc::smem_u32(&S->pv_done[(c - 1) & 1u]), ((c - 1) >> 1) & 1u, abort, status);
+          tc::fence_after_sync();
+          const float alpha = m_new > m_run ? tc::ex2(m_run - m_new) : 1.f;
+          if (ok) {
+            for (int cc = 0; cc < 8; ++cc) {
+              float ov[32];
+              tc::tmem_ld32(tmem + lane_base + kPtTmemO + 32 * cc, ov);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) ov[i] *= alpha;
+              tc::tmem_st32(tmem + lane_base + kPtTmemO + 32 * cc, ov);
+            }
+            tc::tmem_wait_st();
+          }
+          tc::fence_before_sync();
+          l_run *= alpha;
+        }
+        m_run = m_new;
+        if (half == 0) S->ref[h] = m_new;
+      }
+      if (e.w & kPtEnd) break;
       const int row = e.z, part = (e.w >> 8) - 1;
       if (e.w & kPtEmpty) {                        // no page of the segment holds a token
-        if (head < a.H) {
+        if (head < a.H && g == 0) {
           if (part < 0) {
-            __nv_bfloat16 *o = out + ((int64_t)row * a.H + head) * kPtDv + ocol;
-            for (int i = 0; i < 128; i += 8) *reinterpret_cast<uint4 *>(o + i) = make_uint4(0, 0, 0, 0);
-            if (a.o.lse && ocol == 0) a.o.lse[(int64_t)row * a.H + head] = -INFINITY;
+            __nv_bfloat16 *o = out + ((int64_t)row * a.H + head) * kPtDv + 256 * half;
+            for (int i = 0; i < 256; i += 8) *reinterpret_cast<uint4 *>(o + i) = make_uint4(0, 0, 0, 0);
+            if (a.o.lse && half == 0) a.o.lse[(int64_t)row * a.H + head] = -INFINITY;
           } else {
-            float *o = a.o.part_o + ((int64_t)part * a.H + head) * kPtDv + ocol;
-            for (int i = 0; i < 128; i += 4) *reinterpret_cast<float4 *>(o + i) = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (ocol == 0) a.o.part_lse[(int64_t)part * a.H + head] = -INFINITY;
+            float *o = a.o.part_o + ((int64_t)part * a.H + head) * kPtDv + 256 * half;
+            for (int i = 0; i < 256; i += 4) *reinterpret_cast<float4 *>(o + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (half == 0) a.o.part_lse[(int64_t)part * a.H + head] = -INFINITY;
           }
         }
         continue;
       }
-      const bool first = e.w & kPtFirst;
-      if (first) {
-        m_run = -INFINITY;
-        l_run = 0.f;
-      }
-      bool ok = tc::mbar_wait_cl_w(tc::smem_u32(&S->s_full[c & 1u]), (c >> 1) & 1u, abort, status);
-      tc::fence_after_sync();
-      float sv[16];
-      pt_tmem_ld16(tmem + lane_base + kPtTmemS + kPtHalf * (c & 1u) + 16 * sub, sv);
-      tc::tmem_wait_ld();
-      const int valid = ok ? e.y - tok0 : 0;
-      float mx = -INFINITY;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&S->dec[g]));
+      // P = exp2(z - ref) in bf16 into the 128-byte-swizzled A operand; masked tokens hold -inf and give 0
+      const float m_use = m_run == -INFINITY ? 0.f : m_run;
+      uint32_t pw[16];
+      float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        sv[i] = i < valid ? sv[i] * a.scale_log2 : -INFINITY;
-        mx = fmaxf(mx, sv[i]);
+        const float p0 = tc::ex2(fmaf(sv[2 * i], a.scale_log2, -m_use)), p1 = tc::ex2(fmaf(sv[2 * i + 1], a.scale_log2, -m_use));
+        ls[i & 3] += p0 + p1;
+        const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+        pw[i] = *reinterpret_cast<const uint32_t *>(&pb);
       }
-      const float mloc = fmaxf(m_run, mx);
-      S->xm[c & 1u][threadIdx.x] = mloc;
-      tc::named_bar_sync(2, kPtSoftmax);
-      const float *xm = S->xm[c & 1u];
-      const float m_new = fmaxf(fmaxf(mloc, xm[threadIdx.x ^ 64]), fmaxf(xm[threadIdx.x ^ 128], xm[threadIdx.x ^ 192]));
-      if (first) {
-        m_run = m_new;
-      } else {
-        // TMEM accesses are warp-collective: the warp rescales if any of its rows needs it, rows that do not keep their
-        // reference (alpha = 1).  P V of the previous page must have finished before O is touched.
-        const bool want = m_new > m_run + kPtRescale;
-        if (__any_sync(0xffffffffu, want)) {
-          const uint32_t cp = c - 1;
-          ok = tc::mbar_wait_cl_w(tc::smem_u32(&S->pv_done[cp & 1u]), (cp >> 1) & 1u, abort, status) && ok;
-          tc::fence_after_sync();
-          const float alpha = want ? tc::ex2(m_run - m_new) : 1.f;
-          if (ok) {
-            for (int cc = 0; cc < 4; ++cc) {
-              float ov[32];
-              tc::tmem_ld32(tmem + lane_base + kPtTmemO + 128 * sub + 32 * cc, ov);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) ov[i] *= alpha;
-              tc::tmem_st32(tmem + lane_base + kPtTmemO + 128 * sub + 32 * cc, ov);
-            }
-            tc::tmem_wait_st();
-          }
-          if (want) {
-            l_run *= alpha;
-            m_run = m_new;
-          }
-        }
-      }
-      // this P buffer was last read by P V of page c - 2
-      if (c >= 2) ok = tc::mbar_wait_cl_w(tc::smem_u32(&S->pv_done[c & 1u]), ((c >> 1) & 1u) ^ 1u, abort, status) && ok;
-      // P = exp2(z - m) in bf16 into the 128-byte-swizzled A operand; masked tokens hold -inf and give 0
+      l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      // the P buffer was last read by P V of the page before, or by the epilogue of the segment before
+      if (c > 0) ok = pt_wait(tc::smem_u32(&S->pv_done[(c - 1) & 1u]), ((c - 1) >> 1) & 1u, abort, status) && ok;
+      if (first && seg > 0) ok = pt_wait(tc::smem_u32(&S->st_free), (seg - 1) & 1u, abort, status) && ok;
       if (ok) {
-        const float m_use = m_run == -INFINITY ? 0.f : m_run;
-        uint8_t *pbuf = sP + (c & 1u) * kPtP + h * 128;
-        float ls[2] = {0.f, 0.f};
+        uint8_t *pbuf = sP + h * 128;
 #pragma unroll
-        for (int q8 = 0; q8 < 2; ++q8) {
-          uint32_t w4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t0 = 8 * q8 + 2 * i;
-            const float p0 = tc::ex2(sv[t0] - m_use), p1 = tc::ex2(sv[t0 + 1] - m_use);
-            ls[q8] += p0 + p1;
-            const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
-            w4[i] = *reinterpret_cast<const uint32_t *>(&pb);
-          }
-          const int kc = tok0 / 8 + q8;
-          *reinterpret_cast<uint4 *>(pbuf + ((kc ^ (h & 7)) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-        }
-        l_run += ls[0] + ls[1];
+        for (int q8 = 0; q8 < 4; ++q8)
+          *reinterpret_cast<uint4 *>(pbuf + (((4 * half + q8) ^ (h & 7)) << 4)) =
+              make_uint4(pw[4 * q8], pw[4 * q8 + 1], pw[4 * q8 + 2], pw[4 * q8 + 3]);
       }
       tc::fence_proxy_async();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) {
-        if (rank == 0) tc::mbar_arrive(tc::smem_u32(&S->p_full[c & 1u]));
-        else tc::mbar_arrive_remote(p_full_r0 + (c & 1u) * 8);
+        if (rank == 0) tc::mbar_arrive(tc::smem_u32(&S->p_full));
+        else tc::mbar_arrive_remote(p_full_r0);
       }
       ++c;
-      if (!(e.w & kPtLast)) continue;
+      if (!last) continue;
 
-      // ---- epilogue: wait for the last P V, normalise, store through a per-warp staging tile
-      const uint32_t cl = c - 1;
-      ok = tc::mbar_wait_cl_w(tc::smem_u32(&S->pv_done[cl & 1u]), (cl >> 1) & 1u, abort, status) && ok;
+      // ---- epilogue: wait for the last P V, add up the sums, normalise and store
+      ok = pt_wait(tc::smem_u32(&S->pv_done[(c - 1) & 1u]), ((c - 1) >> 1) & 1u, abort, status) && ok;
+      ok = pt_wait(tc::smem_u32(&S->l_ready[seg & 1u]), (seg >> 1) & 1u, abort, status) && ok;
       tc::fence_after_sync();
-      S->xl[threadIdx.x] = l_run;
-      tc::named_bar_sync(2, kPtSoftmax);
-      const float l_tot = (l_run + S->xl[threadIdx.x ^ 64]) + (S->xl[threadIdx.x ^ 128] + S->xl[threadIdx.x ^ 192]);
+      S->x[g][L] = l_run + S->lp[seg & 1u][L];
+      tc::named_bar_sync(1 + g, kPtGroup);
+      const float l_tot = S->x[g][h] + S->x[g][h + 64];
       const float inv = l_tot != 0.f ? 1.f / l_tot : 0.f;
       if (ok) {
-        // both P buffers are free once the last P V finished: each warp stages a 32 x 16 fp32 tile (row = lane, 16-byte
-        // group j at j ^ (row / 2 & 3)) and writes whole 64-byte row segments
-        float *stg = reinterpret_cast<float *>(sP) + warp * 512;
-        const int head0 = 64 * (int)rank + 32 * (warp & 1);
+        // bf16 results go out as they are (64 bytes per lane and step); partial ones through a per-warp tile of 32 rows x 16
+        // entries in the P buffer (16-byte group j of a row at j ^ (row / 2 & 3)), in 64-byte pieces of rows
+        float *stg = reinterpret_cast<float *>(sP) + (warp & 3) * 512;
+        const int head0 = 64 * (int)rank + 32 * (warp & 1), col0 = 256 * half;
         if (head0 < a.H) {
           for (int cc = 0; cc < 8; ++cc) {
-            float ov[16];
-            pt_tmem_ld16(tmem + lane_base + kPtTmemO + 128 * sub + 16 * cc, ov);
+            float ov[32];
+            tc::tmem_ld32(tmem + lane_base + kPtTmemO + 32 * cc, ov);
             tc::tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<float4 *>(stg + lane * 16 + 4 * (j ^ ((lane >> 1) & 3))) =
-                  make_float4(ov[4 * j] * inv, ov[4 * j + 1] * inv, ov[4 * j + 2] * inv, ov[4 * j + 3] * inv);
-            __syncwarp();
+            const int col = col0 + 32 * cc;
             if (part < 0) {
+              __nv_bfloat16 *o = out + ((int64_t)row * a.H + head) * kPtDv + col;
+              if (head < a.H) {
 #pragma unroll
-              for (int it = 0; it < 2; ++it) {
-                const int r = 16 * it + (lane >> 1), j0 = 2 * (lane & 1), x = (r >> 1) & 3;
-                const float4 f0 = *reinterpret_cast<const float4 *>(stg + r * 16 + 4 * (j0 ^ x));
-                const float4 f1 = *reinterpret_cast<const float4 *>(stg + r * 16 + 4 * ((j0 + 1) ^ x));
-                const __nv_bfloat162 b0 = __floats2bfloat162_rn(f0.x, f0.y), b1 = __floats2bfloat162_rn(f0.z, f0.w);
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(f1.x, f1.y), b3 = __floats2bfloat162_rn(f1.z, f1.w);
-                uint4 w;
-                w.x = *reinterpret_cast<const uint32_t *>(&b0);
-                w.y = *reinterpret_cast<const uint32_t *>(&b1);
-                w.z = *reinterpret_cast<const uint32_t *>(&b2);
-                w.w = *reinterpret_cast<const uint32_t *>(&b3);
-                if (head0 + r < a.H)
-                  *reinterpret_cast<uint4 *>(out + ((int64_t)row * a.H + head0 + r) * kPtDv + ocol + 16 * cc + 4 * j0) = w;
+                for (int q8 = 0; q8 < 4; ++q8) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(ov[8 * q8 + 2 * i] * inv, ov[8 * q8 + 2 * i + 1] * inv);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&b);
+                  }
+                  *reinterpret_cast<uint4 *>(o + 8 * q8) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
               }
             } else {
 #pragma unroll
-              for (int it = 0; it < 4; ++it) {
-                const int r = 8 * it + (lane >> 2), j = lane & 3;
-                if (head0 + r < a.H)
-                  *reinterpret_cast<float4 *>(a.o.part_o + ((int64_t)part * a.H + head0 + r) * kPtDv + ocol + 16 * cc + 4 * j) =
-                      *reinterpret_cast<const float4 *>(stg + r * 16 + 4 * (j ^ ((r >> 1) & 3)));
+              for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float *f = ov + 16 * hh + 4 * j;
+                  *reinterpret_cast<float4 *>(stg + lane * 16 + 4 * (j ^ ((lane >> 1) & 3))) =
+                      make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                  const int r = 8 * it + (lane >> 2), j = lane & 3;
+                  if (head0 + r < a.H)
+                    *reinterpret_cast<float4 *>(a.o.part_o + ((int64_t)part * a.H + head0 + r) * kPtDv + col + 16 * hh + 4 * j) =
+                        *reinterpret_cast<const float4 *>(stg + r * 16 + 4 * (j ^ ((r >> 1) & 3)));
+                }
+                __syncwarp();
               }
             }
-            __syncwarp();
           }
         }
-        if (ocol == 0 && head < a.H) {
+        if (half == 0 && head < a.H) {
           const float lse = l_tot != 0.f ? (m_run + __log2f(l_tot)) * 0.69314718055994531f : -INFINITY;
           if (part >= 0) a.o.part_lse[(int64_t)part * a.H + head] = lse;
           else if (a.o.lse) a.o.lse[(int64_t)row * a.H + head] = lse;
@@ -536,9 +606,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) {
+        tc::mbar_arrive(tc::smem_u32(&S->st_free));
         if (rank == 0) tc::mbar_arrive(tc::smem_u32(&S->o_empty));
         else tc::mbar_arrive_remote(o_empty_r0);
       }
+      ++seg;
     }
   }
 
@@ -566,13 +638,13 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn encode_tiled_fn();
 
-static bool pt_map(CUtensorMap *m, const void *base, uint32_t rank, uint64_t d1, uint64_t d2, uint32_t box1) {
+// bf16, [d2][d1][d0] with strides s1, s2 (entries), in boxes of b2 x b1 x 64 entries, 128-byte swizzle
+static bool pt_map(CUtensorMap *m, const void *base, uint32_t rank, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
+                   uint64_t s2, uint32_t b1, uint32_t b2) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)kPtD, d1, d2};
-  cuuint64_t strides[2] = {(cuuint64_t)kPtD * 2, (cuuint64_t)kPtD * 2 * d1};
-  cuuint32_t box[3] = {64, box1, 1};
-  cuuint32_t es[3] = {1, 1, 1};
+  cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1 * 2, s2 * 2};
+  cuuint32_t box[3] = {64, b1, b2}, es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -582,14 +654,16 @@ static bool pt_map(CUtensorMap *m, const void *base, uint32_t rank, uint64_t d1,
 dsa_status_t paged_mla_launch(const void *q, const void *kv, int H, float softmax_scale, const PagedView &view,
                               const PagedOut &o, int max_workers, cudaStream_t stream, int num_sms, int *workers) {
   PtArgs a{view, o, (const __nv_bfloat16 *)kv, H, softmax_scale * 1.4426950408889634f, 2};
-  CUtensorMap tm_q, tm_tiles, tm_rows;
-  const uint64_t rows = (uint64_t)view.num_blocks * kPage;
-  if (!pt_map(&tm_q, q, 3, (uint64_t)H, (uint64_t)view.T, 64) || !pt_map(&tm_tiles, kv, 2, rows, 1, kPtHalf) ||
-      !pt_map(&tm_rows, kv, 2, rows, 1, 1)) {
+  PtMaps tm;
+  const uint64_t rows = (uint64_t)view.num_blocks * kPage, D = kPtD;
+  if (!pt_map(&tm.q, q, 3, D, (uint64_t)H, (uint64_t)view.T, D, D * H, 64, 1) ||
+      !pt_map(&tm.keys, kv, 3, 64, rows, 9, D, 64, kPtHalf, 9) || !pt_map(&tm.values, kv, 3, 64, rows, 9, D, 64, kPtHalf, 4) ||
+      !pt_map(&tm.row, kv, 2, D, rows, 1, D, 0, 1, 1)) {
     set_error("paged attention: cuTensorMapEncodeTiled failed");
     return DSA_ERR_CUDA;
   }
-  const size_t smem = 1024 + kPtQ + kPtNBuf * kPtBuf + 2 * kPtP + sizeof(PtSmem);
+  constexpr size_t smem = kPtQ + kPtNBuf * kPtBuf + kPtP + sizeof(PtSmem);
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   // as many CTA pairs as can be resident at once, found once per device (threads that race on the first call
   // compute the same number)
   static std::atomic<int> resident[kMaxDevices];
@@ -624,8 +698,7 @@ dsa_status_t paged_mla_launch(const void *q, const void *kv, int H, float softma
     resident[dev].store(pairs, std::memory_order_relaxed);
   }
   *workers = std::min(pairs, max_workers);
-  DSA_LAUNCH_PDL("paged_mla_kernel", paged_mla_kernel, dim3(2 * *workers), dim3(kPtThreads), smem, stream, tm_q, tm_tiles,
-                 tm_rows, a);
+  DSA_LAUNCH_PDL("paged_mla_kernel", paged_mla_kernel, dim3(2 * *workers), dim3(kPtThreads), smem, stream, tm, a);
   return DSA_OK;
 }
 
