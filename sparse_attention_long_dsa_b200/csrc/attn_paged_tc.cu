@@ -31,12 +31,11 @@ namespace dsa {
 
 constexpr int kPtD = 576, kPtDv = 512;
 constexpr int kPtHalf = kPage / 2;
-constexpr int kPtNBuf = 4;                         // page buffers
-constexpr int kPtNS = 3;                           // score tiles: QK^T runs kPtNS - 1 pages ahead of P V
+constexpr int kPtNBuf = 4;                         // page buffers, and score tiles
 constexpr int kPtRing = 8;                         // published pages in flight
-constexpr int kPtThreads = 384;                    // softmax x 8, keys, MMA, resolve, values
+constexpr int kPtThreads = 384;                    // softmax x 8, keys, QK^T, P V, values
 constexpr int kPtGroup = 128;                      // threads of a softmax group (4 warps)
-constexpr int kPtWarpKeys = 8, kPtWarpMMA = 9, kPtWarpResolve = 10, kPtWarpValues = 11;
+constexpr int kPtWarpKeys = 8, kPtWarpQK = 9, kPtWarpPV = 10, kPtWarpValues = 11;
 constexpr uint32_t kPtBlk = kPtHalf * 128;         // one 64-entry block of a CTA's 32 tokens: 4 KB
 constexpr uint32_t kPtBuf = 9 * kPtBlk;
 constexpr uint32_t kPtQ = 9 * 8192;
@@ -50,10 +49,10 @@ struct PtSmem {
   uint64_t buf_empty[kPtNBuf];      // MMA commit to both CTAs after P V
   uint64_t v_full[kPtNBuf];         // rank 0: bytes of both CTAs' peer values
   uint64_t q_full, q_empty;
-  uint64_t s_full[kPtNS];
+  uint64_t s_full[kPtNBuf];
   uint64_t p_full;
   uint64_t pv_done[2];              // by page parity: a group waits for every phase of the other group's barrier
-  uint64_t o_empty, drain;
+  uint64_t o_empty, drain[2];
   uint64_t ent_full[kPtRing], ent_empty[kPtRing];
   uint32_t tmem_base;
   int abort;
@@ -188,8 +187,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       tc::mbar_init(tc::smem_u32(&S->buf_full[i]), 1);
       tc::mbar_init(tc::smem_u32(&S->buf_empty[i]), 1);
       tc::mbar_init(tc::smem_u32(&S->v_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&S->s_full[i]), 1);
     }
-    for (int i = 0; i < kPtNS; ++i) tc::mbar_init(tc::smem_u32(&S->s_full[i]), 1);
     tc::mbar_init(tc::smem_u32(&S->p_full), 8);
     tc::mbar_init(tc::smem_u32(&S->st_free), 4);
     for (int i = 0; i < 2; ++i) {
@@ -200,10 +199,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     tc::mbar_init(tc::smem_u32(&S->q_full), 1);
     tc::mbar_init(tc::smem_u32(&S->q_empty), 1);
     tc::mbar_init(tc::smem_u32(&S->o_empty), 8);
-    tc::mbar_init(tc::smem_u32(&S->drain), 1);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(tc::smem_u32(&S->drain[i]), 1);
     for (int i = 0; i < kPtRing; ++i) {
       tc::mbar_init(tc::smem_u32(&S->ent_full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&S->ent_empty[i]), rank == 0 ? 11 : 10);   // softmax x 8, keys, values, MMA (rank 0)
+      tc::mbar_init(tc::smem_u32(&S->ent_empty[i]), rank == 0 ? 11 : 9);   // softmax x 8, values, QK^T and P V (rank 0)
     }
     S->abort = 0;
     tc::fence_barrier_init();
@@ -212,7 +211,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     tc::prefetch_tmap(&tm.values);
     tc::prefetch_tmap(&tm.row);
   }
-  if (warp == kPtWarpMMA) {
+  if (warp == kPtWarpPV) {
     tc::tmem_alloc2(tc::smem_u32(&S->tmem_base), 512);
     tc::tmem_relinquish2();
   }
@@ -240,22 +239,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     return true;
   };
 
-  if (warp == kPtWarpResolve) {
-    // ====================================================================== resolve
+  if (warp == kPtWarpKeys) {
+    // ====================================================================== pages, keys and q
     if (lane == 0 && rank == 0) a.o.info[pair] = worker_info(a.view, S->plan);
-    uint32_t ec = 0;
-    auto push = [&](int phys, int ntok, int row, int info) {
+    const int oob = a.view.num_blocks * kPage;             // a row outside the map: zero-filled
+    const uint32_t buf_full_r0 = tc::map_to_rank(tc::smem_u32(&S->buf_full[0]), 0);
+    const uint32_t q_full_r0 = tc::map_to_rank(tc::smem_u32(&S->q_full), 0);
+    uint32_t ec = 0, c = 0, v = 0;
+    auto publish = [&](int phys, int ntok, int row, int info) -> bool {
       const uint32_t slot = ec % kPtRing;
-      const bool ok = pt_wait(tc::smem_u32(&S->ent_empty[slot]), ((ec / kPtRing) & 1u) ^ 1u, abort, status);
-      if (lane == 0 && ok) {
+      if (!pt_wait(tc::smem_u32(&S->ent_empty[slot]), ((ec / kPtRing) & 1u) ^ 1u, abort, status)) return false;
+      if (lane == 0) {
         S->ent[slot] = make_int4(phys, ntok, row, info);
         tc::mbar_arrive(tc::smem_u32(&S->ent_full[slot]));
-        const int t0 = kPtHalf * (int)rank, n = min(kPtHalf, ntok - t0);
-        if (n > 0) tc::prefetch_l2(a.kv + ((int64_t)phys + t0) * kPtD, (uint32_t)n * kPtD * 2);
       }
       __syncwarp();
       ++ec;
-      return ok;
+      return true;
+    };
+    auto page = [&](int phys, int ntok, int row, int info) -> bool {
+      if (!publish(phys, ntok, row, info)) return false;
+      const uint32_t b = c % kPtNBuf;
+      if (!pt_wait(tc::smem_u32(&S->buf_empty[b]), ((c / kPtNBuf) & 1u) ^ 1u, abort, status)) return false;
+      if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->buf_full[b]), 2u * kPtBuf);
+      __syncwarp();
+      pt_copy(&tm.keys, &tm.row, lane, phys, ntok, kPtHalf * (int)rank, oob, 0, 9, tc::smem_u32(sBuf + b * kPtBuf),
+              buf_full_r0 + b * 8);
+      if (info & kPtFirst) {
+        // q is overwritten once the previous segment's last QK^T has run
+        if (v > 0 && !pt_wait(tc::smem_u32(&S->q_empty), (v - 1) & 1u, abort, status)) return false;
+        if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->q_full), 2u * kPtQ);
+        __syncwarp();
+        if (lane < 9) pt_load_3d_pair(tc::smem_u32(sQ + lane * 8192), &tm.q, lane * 64, 64 * (int)rank, row, q_full_r0);
+        ++v;
+      }
+      ++c;
+      return true;
     };
     SegmentWalk walk(S->plan);
     int row, sa, sb, part;
@@ -263,51 +282,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     while (ok && walk.next(a.view, S->plan, pair, &row, &sa, &sb, &part)) {
       const int n = row_tokens(a.view, row, status);
       const int tag = (part + 1) << 8;
-      int flags = kPtFirst, h_phys = 0, h_ntok = 0;        // one page is held back until it is known whether another follows
+      // 32 slots per load, the next 32 loaded ahead; one page is held back until it is known whether another follows
+      int flags = kPtFirst, h_phys = 0, h_ntok = 0, blk = 0, nt = 0;
+      if (sa + lane < sb) nt = slot_tokens(a.view, row, n, sa + lane, &blk, status);
       for (int s0 = sa; s0 < sb && ok; s0 += 32) {
-        int blk = 0, nt = 0;
-        if (s0 + lane < sb) nt = slot_tokens(a.view, row, n, s0 + lane, &blk, status);
+        int blk_n = 0, nt_n = 0;
+        if (s0 + 32 + lane < sb) nt_n = slot_tokens(a.view, row, n, s0 + 32 + lane, &blk_n, status);
         uint32_t have = __ballot_sync(0xffffffffu, nt > 0);
         while (have && ok) {
           const int l = __ffs(have) - 1;
           have &= have - 1;
           if (h_ntok) {
-            ok = push(h_phys, h_ntok, row, flags | tag);
+            ok = page(h_phys, h_ntok, row, flags | tag);
             flags = 0;
           }
           h_phys = __shfl_sync(0xffffffffu, blk, l) * kPage;
           h_ntok = __shfl_sync(0xffffffffu, nt, l);
         }
+        blk = blk_n;
+        nt = nt_n;
       }
-      if (ok) ok = push(h_phys, h_ntok, row, (h_ntok ? flags | kPtLast : kPtEmpty) | tag);
+      if (ok) ok = h_ntok ? page(h_phys, h_ntok, row, flags | kPtLast | tag) : publish(0, 0, row, kPtEmpty | tag);
     }
-    if (ok) push(0, 0, 0, kPtEnd);
-  } else if (warp == kPtWarpKeys) {
-    // ====================================================================== keys and q
-    const int oob = a.view.num_blocks * kPage;             // a row outside the map: zero-filled
-    const uint32_t buf_full_r0 = tc::map_to_rank(tc::smem_u32(&S->buf_full[0]), 0);
-    const uint32_t q_full_r0 = tc::map_to_rank(tc::smem_u32(&S->q_full), 0);
-    uint32_t ec = 0, c = 0, v = 0;
-    int4 e;
-    while (next_entry(ec, &e)) {
-      if (e.w & kPtEnd) break;
-      if (e.w & kPtEmpty) continue;
-      const uint32_t b = c % kPtNBuf;
-      if (!pt_wait(tc::smem_u32(&S->buf_empty[b]), ((c / kPtNBuf) & 1u) ^ 1u, abort, status)) break;
-      if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->buf_full[b]), 2u * kPtBuf);
-      __syncwarp();
-      pt_copy(&tm.keys, &tm.row, lane, e.x, e.y, kPtHalf * (int)rank, oob, 0, 9, tc::smem_u32(sBuf + b * kPtBuf),
-              buf_full_r0 + b * 8);
-      if (e.w & kPtFirst) {
-        // q is overwritten once the previous segment's last QK^T has run
-        if (v > 0 && !pt_wait(tc::smem_u32(&S->q_empty), (v - 1) & 1u, abort, status)) break;
-        if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->q_full), 2u * kPtQ);
-        __syncwarp();
-        if (lane < 9) pt_load_3d_pair(tc::smem_u32(sQ + lane * 8192), &tm.q, lane * 64, 64 * (int)rank, e.z, q_full_r0);
-        ++v;
-      }
-      ++c;
-    }
+    if (ok) publish(0, 0, 0, kPtEnd);
   } else if (warp == kPtWarpValues) {
     // ====================================================================== the peer's values
     const int oob = a.view.num_blocks * kPage;
@@ -320,88 +317,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       if (e.w & kPtEmpty) continue;
       const uint32_t b = c % kPtNBuf;
       // QK^T of this page has read the buffers
-      if (!pt_wait(tc::smem_u32(&S->s_full[c % kPtNS]), (c / kPtNS) & 1u, abort, status)) break;
+      if (!pt_wait(tc::smem_u32(&S->s_full[c % kPtNBuf]), (c / kPtNBuf) & 1u, abort, status)) break;
       if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->v_full[b]), 2u * 4u * kPtBlk);
       __syncwarp();
       pt_copy(&tm.values, &tm.row, lane, e.x, e.y, kPtHalf * (int)(rank ^ 1u), oob, src, 4,
               tc::smem_u32(sBuf + b * kPtBuf + dst * kPtBlk), v_full_r0 + b * 8);
       ++c;
     }
-  } else if (warp == kPtWarpMMA) {
-    // ====================================================================== MMA issuer (rank 0, whole warp)
+  } else if (warp == kPtWarpQK || warp == kPtWarpPV) {
+    // ====================================================================== MMA issuers (rank 0, whole warps)
+    // Two warps, because issuing a page's MMAs and waiting for its operands takes one warp longer (about 1,900 cycles) than
+    // the tensor core needs to run them (1,425).  A page's score tile is free when its buffer is.
     if (rank == 0) {
-      constexpr uint32_t idesc_qk = tc::make_idesc(1, 1, 128, kPage, false, false);
-      constexpr uint32_t idesc_pv = tc::make_idesc(1, 1, 128, 256, false, true);
       const uint16_t both = 3;
-      const uint64_t q_desc = tc::desc_sw128(tc::smem_u32(sQ), 1024);
-      const uint64_t p_desc = tc::desc_sw128(tc::smem_u32(sP), 1024);
-      const uint64_t kv_desc = tc::desc_sw128(tc::smem_u32(sBuf), 1024);
-      const uint64_t v_desc = tc::desc_sw128_lbo(tc::smem_u32(sBuf), kPtBlk, 1024);
-      const uint32_t tm_o = __shfl_sync(0xffffffffu, tmem + kPtTmemO, 0);
-      uint32_t ec = 0, c = 0, done = 0, segs = 0, segs_pv = 0;      // pages with QK^T, with P V; segments begun
-      uint32_t firsts = 0;                                          // bit i: page c - 1 - i begins a segment
-      auto pv = [&]() -> bool {                                     // P V of page `done`
-        const bool first = (firsts >> (c - done - 1)) & 1u;
-        const uint32_t b = done % kPtNBuf;
-        if (!pt_wait_cl(tc::smem_u32(&S->p_full), done & 1u, abort, status)) return false;
-        if (!pt_wait(tc::smem_u32(&S->v_full[b]), (done / kPtNBuf) & 1u, abort, status)) return false;
-        if (first) {
-          if (segs_pv > 0 && !pt_wait_cl(tc::smem_u32(&S->o_empty), (segs_pv - 1) & 1u, abort, status)) return false;
-          ++segs_pv;
-        }
-        tc::fence_after_sync();
-        const uint64_t vb = v_desc + ((b * kPtBuf) >> 4);
-        if (pt_elect()) {
-          // K steps of 16 tokens: token half (4 blocks apart) x two steps of 16 rows
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              pt_mma_pair(tm_o + 128 * p, p_desc + 2 * k,
-                          vb + ((2 * p * kPtBlk + (k >> 1) * 4 * kPtBlk + (k & 1) * 16 * 128) >> 4), idesc_pv, k > 0 || !first);
-        }
-        __syncwarp();
-        tc::mma_commit_pair_w(tc::smem_u32(&S->buf_empty[b]), both);
-        tc::mma_commit_pair_w(tc::smem_u32(&S->pv_done[done & 1u]), both);
-        ++done;
-        return true;
-      };
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      uint32_t ec = 0, c = 0, segs = 0;
       int4 e;
-      bool ok = true;
-      while (ok && (ok = next_entry(ec, &e))) {
-        const int info = __shfl_sync(0xffffffffu, e.w, 0);
-        if (info & kPtEnd) break;
-        if (info & kPtEmpty) {
-          // A run of these may fill the ring before the next page, and the softmax frees it only after the P V it waits for.
-          while (ok && done < c) ok = pv();
-          continue;
-        }
-        const uint32_t b = c % kPtNBuf;
-        if (info & kPtFirst) ok = pt_wait(tc::smem_u32(&S->q_full), segs++ & 1u, abort, status);
-        if (ok) ok = pt_wait(tc::smem_u32(&S->buf_full[b]), (c / kPtNBuf) & 1u, abort, status);
-        if (!ok) break;
-        tc::fence_after_sync();
-        // score tile c % kPtNS: read before P V of page c - kPtNS was issued
-        const uint64_t kb = kv_desc + ((b * kPtBuf) >> 4);
-        const uint32_t d = tm_o + kPtTmemS - kPtTmemO + kPtHalf * (c % kPtNS);
-        if (pt_elect()) {
+      const int which = warp == kPtWarpPV;
+      if (which == 0) {
+        constexpr uint32_t idesc = tc::make_idesc(1, 1, 128, kPage, false, false);
+        const uint64_t q_desc = tc::desc_sw128(tc::smem_u32(sQ), 1024);
+        const uint64_t kv_desc = tc::desc_sw128(tc::smem_u32(sBuf), 1024);
+        while (next_entry(ec, &e)) {
+          const int info = __shfl_sync(0xffffffffu, e.w, 0);
+          if (info & kPtEnd) break;
+          if (info & kPtEmpty) continue;
+          const uint32_t b = c % kPtNBuf;
+          if ((info & kPtFirst) && !pt_wait(tc::smem_u32(&S->q_full), segs++ & 1u, abort, status)) break;
+          if (!pt_wait(tc::smem_u32(&S->buf_full[b]), (c / kPtNBuf) & 1u, abort, status)) break;
+          tc::fence_after_sync();
+          const uint64_t kb = kv_desc + ((b * kPtBuf) >> 4);
+          const uint32_t d = tm + kPtTmemS + kPtHalf * b;
+          if (pt_elect()) {
 #pragma unroll
-          for (int i = 0; i < 9; ++i)
+            for (int i = 0; i < 9; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              pt_mma_pair(d, q_desc + ((i * 8192) >> 4) + 2 * k, kb + ((i * kPtBlk) >> 4) + 2 * k, idesc_qk, i + k > 0);
+              for (int k = 0; k < 4; ++k)
+                pt_mma_pair(d, q_desc + ((i * 8192) >> 4) + 2 * k, kb + ((i * kPtBlk) >> 4) + 2 * k, idesc, i + k > 0);
+          }
+          __syncwarp();
+          tc::mma_commit_pair_w(tc::smem_u32(&S->s_full[b]), both);
+          if (info & kPtLast) tc::mma_commit_pair_w(tc::smem_u32(&S->q_empty), both);
+          ++c;
         }
-        __syncwarp();
-        tc::mma_commit_pair_w(tc::smem_u32(&S->s_full[c % kPtNS]), both);
-        if (info & kPtLast) tc::mma_commit_pair_w(tc::smem_u32(&S->q_empty), both);
-        firsts = firsts << 1 | (uint32_t)(info & kPtFirst);
-        ++c;
-        if (c - done == kPtNS) ok = pv();
+      } else {
+        constexpr uint32_t idesc = tc::make_idesc(1, 1, 128, 256, false, true);
+        const uint64_t p_desc = tc::desc_sw128(tc::smem_u32(sP), 1024);
+        const uint64_t v_desc = tc::desc_sw128_lbo(tc::smem_u32(sBuf), kPtBlk, 1024);
+        while (next_entry(ec, &e)) {
+          const int info = __shfl_sync(0xffffffffu, e.w, 0);
+          if (info & kPtEnd) break;
+          if (info & kPtEmpty) continue;
+          const uint32_t b = c % kPtNBuf;
+          const bool first = info & kPtFirst;
+          if (first) {
+            if (segs > 0 && !pt_wait_cl(tc::smem_u32(&S->o_empty), (segs - 1) & 1u, abort, status)) break;
+            ++segs;
+          }
+          if (!pt_wait(tc::smem_u32(&S->v_full[b]), (c / kPtNBuf) & 1u, abort, status)) break;
+          if (!pt_wait_cl(tc::smem_u32(&S->p_full), c & 1u, abort, status)) break;
+          tc::fence_after_sync();
+          const uint64_t vb = v_desc + ((b * kPtBuf) >> 4);
+          if (pt_elect()) {
+            // K steps of 16 tokens: token half (4 blocks apart) x two steps of 16 rows
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                pt_mma_pair(tm + kPtTmemO + 128 * p, p_desc + 2 * k,
+                            vb + ((2 * p * kPtBlk + (k >> 1) * 4 * kPtBlk + (k & 1) * 16 * 128) >> 4), idesc, k > 0 || !first);
+          }
+          __syncwarp();
+          tc::mma_commit_pair_w(tc::smem_u32(&S->buf_empty[b]), both);
+          tc::mma_commit_pair_w(tc::smem_u32(&S->pv_done[c & 1u]), both);
+          ++c;
+        }
       }
-      while (ok && done < c) ok = pv();
-      tc::mma_commit_pair_local_w(tc::smem_u32(&S->drain));
+      tc::mma_commit_pair_local_w(tc::smem_u32(&S->drain[which]));
       volatile int no_abort = 0;
-      __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&S->drain), 0, &no_abort, status));
+      __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&S->drain[which]), 0, &no_abort, status));
     }
   } else {
     // ====================================================================== softmax + epilogue (two groups of 4 warps)
@@ -441,9 +435,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       float sv[kPtHalf];
       float mx = -INFINITY;
       if (page) {
-        ok = pt_wait(tc::smem_u32(&S->s_full[c % kPtNS]), (c / kPtNS) & 1u, abort, status);
+        ok = pt_wait(tc::smem_u32(&S->s_full[c % kPtNBuf]), (c / kPtNBuf) & 1u, abort, status);
         tc::fence_after_sync();
-        tc::tmem_ld32(tmem + lane_base + kPtTmemS + kPtHalf * (c % kPtNS), sv);
+        tc::tmem_ld32(tmem + lane_base + kPtTmemS + kPtHalf * (c % kPtNBuf), sv);
         tc::tmem_wait_ld();
         if (e.y < kPage) {
 #pragma unroll
@@ -618,7 +612,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::cluster_sync();
-  if (warp == kPtWarpMMA) {
+  if (warp == kPtWarpPV) {
     tc::fence_after_sync();
     tc::tmem_dealloc2(tmem, 512);
   }
