@@ -32,6 +32,13 @@ struct PsArgs {
 
 __device__ __forceinline__ void ps_store(float *p, float v) { *p = v; }
 __device__ __forceinline__ void ps_store(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void ps_store4(float *p, const float *v) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void ps_store4(__nv_bfloat16 *p, const float *v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
 
 __host__ __device__ constexpr int ps_stride(int Dqk) { return (Dqk + 3) / 4 * 4 + 4; }
 
@@ -161,91 +168,124 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a, 
 
 // ------------------------------------------------------------------------------------------------ join
 // out[row, h, :] = sum_w exp(lse_w - lse) o_w,  lse = log sum_w exp(lse_w)  over the workers w that hold a part of the row.
-// One CTA per (split row, head); at most min(T, workers) rows are split, and CTA x finds the x-th of them in info.  Four
-// groups of 128 threads take every fourth part each, four loads in flight per thread, and add up in a fixed order: a row
-// over 74 workers is five rounds of loads instead of 74.
-constexpr int kPcGroups = 4, kPcThreads = 128 * kPcGroups, kPcMaxParts = 160;
+// At most min(T, workers) rows are split; CTA x finds the x-th of them in info, a warp takes a head (kGroup = 1) or every
+// kGroup-th part of one (the sums of the kGroup warps are added in a fixed order).  A lane holds kN pieces of the row (four
+// values each where Dv % 4 == 0, else single ones).  Bound by latency: three dependent loads, so it is the number of warps in
+// flight that counts.  Few rows have many parts each: kGroup = 8 up to 1,184 (row, head) pairs, one CTA of 8 warps per head
+// (a 1M-token row, 74 parts of 128 heads: 8 us, 90 us with one warp per head and part after part); more rows have few parts:
+// a warp per head (the 32-row decode batch, 3.3 parts each: 6 us, 28 us with 16 warps per head).
+constexpr int kPcThreads = 256, kPcWarps = kPcThreads / 32, kPcMaxWorkers = 160;
 
-template <typename T>
+template <typename T, int kGroup, int kN, bool kVec>
 __global__ void __launch_bounds__(kPcThreads) paged_combine_kernel(const PagedOut o, int workers, int H, int Dv) {
-  __shared__ float s_w[kPcMaxParts];
-  __shared__ float s_acc[kPcGroups - 1][512];
-  __shared__ int s_last, s_first, s_row;
+  constexpr int kLane = kVec ? 4 : 1, kBlocks = kPcMaxWorkers / 32;
+  __shared__ float s_acc[kGroup > 1 ? kPcWarps : 1][kN * kLane * 32];
   pdl_wait();
   pdl_trigger();
-  const int h = blockIdx.y, tid = threadIdx.x;
-  if (tid < 32) {
-    int seen = 0, last = -1;
-    int2 who = make_int2(-1, 0);
-    for (int w0 = 0; w0 < workers; w0 += 32) {
-      const int2 i = w0 + tid < workers ? __ldg(o.info + w0 + tid) : make_int2(-1, 0);
-      const uint32_t m = __ballot_sync(0xffffffffu, i.x >= 0);
-      const int nth = seen + __popc(m & ((1u << tid) - 1u));
-      const uint32_t me = __ballot_sync(0xffffffffu, i.x >= 0 && nth == (int)blockIdx.x);
-      if (me) {
-        const int l = __ffs(me) - 1;
-        last = w0 + l;
-        who.x = __shfl_sync(0xffffffffu, i.x, l);
-        who.y = __shfl_sync(0xffffffffu, i.y, l);
-        break;
-      }
-      seen += __popc(m);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.y * (kPcWarps / kGroup) + warp / kGroup, sub = warp % kGroup;
+  int2 info[kBlocks];
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i)
+    info[i] = 32 * i + lane < workers ? __ldg(o.info + 32 * i + lane) : make_int2(-1, 0);
+  int last = -1, row = -1, first = 0, seen = 0;
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    const uint32_t m = __ballot_sync(0xffffffffu, info[i].x >= 0);
+    const uint32_t me = __ballot_sync(0xffffffffu, info[i].x >= 0 && seen + __popc(m & ((1u << lane) - 1u)) == (int)blockIdx.x);
+    if (me) {
+      const int l = __ffs(me) - 1;
+      last = 32 * i + l;
+      row = __shfl_sync(0xffffffffu, info[i].x, l);
+      first = __shfl_sync(0xffffffffu, info[i].y, l);
     }
-    if (tid == 0) {
-      s_last = last;
-      s_first = who.y;
-      s_row = who.x;
-    }
+    seen += __popc(m);
   }
-  __syncthreads();
-  const int row = s_row, first = s_first;
-  if (row < 0) return;
-  const int n = s_last - first + 1;
-  // part s: the first worker's odd slot, then the even slots of the workers after it
-  auto slot = [&](int s) { return (int64_t)(2 * (first + s) + (s == 0 ? 1 : 0)) * H + h; };
-  for (int s = tid; s < n; s += kPcThreads) s_w[s] = __ldg(o.part_lse + slot(s));
-  __syncthreads();
-  float mx = -INFINITY;
-  for (int s = 0; s < n; ++s) mx = fmaxf(mx, s_w[s]);
-  float tot = 0.f;
-  if (mx != -INFINITY)
-    for (int s = 0; s < n; ++s) tot += expf(s_w[s] - mx);
-  const float inv = tot != 0.f ? 1.f / tot : 0.f;
-  const int g = tid >> 7, t = tid & 127;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  if (tot != 0.f) {
-    if ((Dv & 3) == 0) {
-      if (4 * t < Dv)
-#pragma unroll 4
-        for (int s = g; s < n; s += kPcGroups) {
-          const float4 v = __ldg(reinterpret_cast<const float4 *>(o.part_o + slot(s) * Dv) + t);
-          const float w = expf(s_w[s] - mx) * inv;
-          acc[0] = fmaf(w, v.x, acc[0]);
-          acc[1] = fmaf(w, v.y, acc[1]);
-          acc[2] = fmaf(w, v.z, acc[2]);
-          acc[3] = fmaf(w, v.w, acc[3]);
+  if (row < 0) return;                             // the same for every warp of the CTA
+  const int n = last - first + 1;
+  const bool live = h < H;
+  float acc[kN * kLane];
+#pragma unroll
+  for (int i = 0; i < kN * kLane; ++i) acc[i] = 0.f;
+  float lse = -INFINITY;
+  if (live) {
+    // part s: the first worker's odd slot, then the even slots of the workers after it
+    auto slot = [&](int s) { return (int64_t)(2 * (first + s) + (s == 0 ? 1 : 0)) * H + h; };
+    float w[kBlocks], mx = -INFINITY, tot = 0.f;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      w[i] = 32 * i + lane < n ? __ldg(o.part_lse + slot(32 * i + lane)) : -INFINITY;
+      mx = fmaxf(mx, w[i]);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      w[i] = mx == -INFINITY ? 0.f : expf(w[i] - mx);
+      tot += w[i];
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, off);
+    const float inv = tot != 0.f ? 1.f / tot : 0.f;
+    lse = tot != 0.f ? mx + logf(tot) : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      if (32 * i >= n) break;
+      const int top = min(32, n - 32 * i);
+#pragma unroll 2
+      for (int l = sub; l < top; l += kGroup) {    // 32 is a multiple of kGroup
+        const float ws = __shfl_sync(0xffffffffu, w[i], l) * inv;
+        const float *p = o.part_o + slot(32 * i + l) * Dv;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+          const int d = (32 * k + lane) * kLane;
+          if (d < Dv) {
+            if (kVec) {
+              const float4 v = __ldg(reinterpret_cast<const float4 *>(p + d));
+              acc[kLane * k] = fmaf(ws, v.x, acc[kLane * k]);
+              acc[kLane * k + kLane / 4] = fmaf(ws, v.y, acc[kLane * k + kLane / 4]);
+              acc[kLane * k + kLane / 2] = fmaf(ws, v.z, acc[kLane * k + kLane / 2]);
+              acc[kLane * k + kLane - 1] = fmaf(ws, v.w, acc[kLane * k + kLane - 1]);
+            } else {
+              acc[k] = fmaf(ws, __ldg(p + d), acc[k]);
+            }
+          }
         }
-    } else {
-#pragma unroll 4
-      for (int s = g; s < n; s += kPcGroups) {
-        const float w = expf(s_w[s] - mx) * inv;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (4 * t + i < Dv) acc[i] = fmaf(w, __ldg(o.part_o + slot(s) * Dv + 4 * t + i), acc[i]);
       }
     }
   }
-  if (g > 0)
-    for (int i = 0; i < 4; ++i) s_acc[g - 1][4 * t + i] = acc[i];
-  __syncthreads();
-  if (g == 0) {
-    T *out = (T *)o.out + ((int64_t)row * H + h) * Dv;
+  if (kGroup > 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (4 * t + i < Dv) ps_store(out + 4 * t + i, (acc[i] + s_acc[0][4 * t + i]) + (s_acc[1][4 * t + i] + s_acc[2][4 * t + i]));
-    }
-    if (o.lse && t == 0) o.lse[(int64_t)row * H + h] = tot != 0.f ? mx + logf(tot) : -INFINITY;
+    for (int i = 0; i < kN * kLane; ++i) s_acc[warp][32 * i + lane] = acc[i];
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int i = 0; i < kN * kLane; ++i)
+      for (int g = 1; g < kGroup; ++g) acc[i] += s_acc[warp + g][32 * i + lane];
   }
+  if (!live) return;
+  T *out = (T *)o.out + ((int64_t)row * H + h) * Dv;
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    const int d = (32 * k + lane) * kLane;
+    if (d >= Dv) continue;
+    if (kVec) ps_store4(out + d, acc + kLane * k);
+    else ps_store(out + d, acc[k]);
+  }
+  if (o.lse && lane == 0) o.lse[(int64_t)row * H + h] = lse;
+}
+
+template <typename T, int kN, bool kVec>
+static dsa_status_t combine_launch(const PagedOut &o, int workers, int T_rows, int H, int Dv, cudaStream_t stream) {
+  const int rows = std::min(workers, T_rows);
+  if ((int64_t)T_rows * H <= 8 * 148) {
+    DSA_LAUNCH_PDL("paged_combine_kernel", (paged_combine_kernel<T, 8, kN, kVec>), dim3(rows, H), dim3(kPcThreads), 0, stream, o,
+                   workers, H, Dv);
+  } else {
+    DSA_LAUNCH_PDL("paged_combine_kernel", (paged_combine_kernel<T, 1, kN, kVec>), dim3(rows, (H + kPcWarps - 1) / kPcWarps),
+                   dim3(kPcThreads), 0, stream, o, workers, H, Dv);
+  }
+  return DSA_OK;
 }
 
 // ------------------------------------------------------------------------------------------------ host
@@ -293,18 +333,15 @@ dsa_status_t paged_attn_launch(const void *q, bool bf16, const void *kv, const v
     int workers = 0;
     const dsa_status_t st = paged_mla_launch(q, kv, H, scale, a.view, a.o, paged_max_workers(Dv), stream, num_sms, &workers);
     if (st != DSA_OK) return st;
-    DSA_LAUNCH_PDL("paged_combine_kernel", paged_combine_kernel<__nv_bfloat16>, dim3(std::min(workers, b->total_q), H),
-                   dim3(kPcThreads), 0, stream, a.o, workers, H, Dv);
-    return DSA_OK;
+    return combine_launch<__nv_bfloat16, 4, true>(a.o, workers, b->total_q, H, Dv, stream);
   }
   const int workers = std::min(num_sms, paged_max_workers(Dv));
   const int D4 = (Dqk + 3) / 4;
   const size_t smem = 4 * ((size_t)kPsHeads * 4 * D4 + (size_t)kPsTok * ps_stride(Dqk) + kPsHeads * kPsTok + (size_t)kPsTok * Dv);
   cudaFuncSetAttribute(paged_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   DSA_LAUNCH_PDL("paged_simt_kernel", paged_simt_kernel, dim3(workers), dim3(kPsThreads), smem, stream, a, 2);
-  DSA_LAUNCH_PDL("paged_combine_kernel", paged_combine_kernel<float>, dim3(std::min(workers, b->total_q), H),
-                 dim3(kPcThreads), 0, stream, a.o, workers, H, Dv);
-  return DSA_OK;
+  if (Dv % 4 == 0) return combine_launch<float, 1, true>(a.o, workers, b->total_q, H, Dv, stream);
+  return combine_launch<float, 4, false>(a.o, workers, b->total_q, H, Dv, stream);
 }
 
 }  // namespace dsa
