@@ -161,7 +161,7 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -290,19 +290,17 @@ def dsa_cp_merge(part_out, dt: int, part_lse, G: int, T: int, H: int, Dv: int, o
                                _stream(stream)), "dsa_cp_merge")
 
 
-def _arg(t, dtypes: tuple, what: str):
-    """A dense tensor of one of the named dtypes on the current device: its address."""
+def _dense(what: str, dtype, *tensors):
+    """Addresses of dense tensors of one dtype on the current device."""
     import torch
-    if str(t.dtype)[6:] not in dtypes:
-        raise DSAError(DSA_ERR_INVALID_ARG, what, f"dtype {t.dtype}; expected {' or '.join(dtypes)}")
-    p = _ptr(t)
-    if t.device.index != torch.cuda.current_device():
-        raise DSAError(DSA_ERR_INVALID_ARG, what, f"a tensor on {t.device}; the current device is "
-                                                  f"cuda:{torch.cuda.current_device()}")
-    return p
-
-
-_INT = ("int32",)
+    cur = torch.cuda.current_device() if tensors[0].is_cuda else -1
+    for t in tensors:
+        if t.dtype is not dtype:
+            raise DSAError(DSA_ERR_INVALID_ARG, what, f"a {t.dtype} tensor; expected {dtype}")
+        if t.get_device() != cur or cur < 0 or not t.is_contiguous():
+            _ptr(t)                                  # names a host or strided tensor
+            raise DSAError(DSA_ERR_INVALID_ARG, what, f"a tensor on {t.device}; the current device is cuda:{cur}")
+    return [t.data_ptr() for t in tensors]
 
 
 def _shape(t, shape: tuple, what: str):
@@ -321,6 +319,7 @@ def dsa_batch_extend(cached_lens, new_lens, page_size: int, num_blocks: int, tot
     """Block tables, slots and positions of a step, from device lengths (cached_lens, new_lens [B]): block_table [B,
     max_blocks] and the stack free_blocks / free_count lose and gain pages on the device.  seq_lens may be cached_lens
     and free_left may be free_count."""
+    import torch
     w = "dsa_batch_extend"
     n = cached_lens.numel()
     _shape(new_lens, (n,), w)
@@ -328,25 +327,26 @@ def dsa_batch_extend(cached_lens, new_lens, page_size: int, num_blocks: int, tot
     _shape(cu_q, (n + 1,), w)
     if block_table.dim() != 2 or block_table.shape[0] != n or slots.numel() < total_q or positions.numel() < total_q:
         raise DSAError(DSA_ERR_INVALID_ARG, w, f"block_table [{n}, max_blocks], slots and positions [total_q] expected")
-    _check(load().dsa_batch_extend(
-        _arg(cached_lens, _INT, w), _arg(new_lens, _INT, w), n, page_size, block_table.shape[1], num_blocks, total_q,
-        _arg(free_blocks, _INT, w), free_blocks.numel(), _arg(free_count, _INT, w), _arg(block_table, _INT, w),
-        _arg(seq_lens, _INT, w), _arg(cu_q, _INT, w), _arg(slots, ("int64",), w), _arg(positions, _INT, w),
-        _arg(free_left, _INT, w), _ptr(ws), ws_bytes, _stream(stream)), w)
+    cached, new, free, count, table, seq, cu, pos, left = _dense(w, torch.int32, cached_lens, new_lens, free_blocks, free_count,
+                                                                 block_table, seq_lens, cu_q, positions, free_left)
+    slot, = _dense(w, torch.int64, slots)
+    _check((_lib or load()).dsa_batch_extend(cached, new, n, page_size, block_table.shape[1], num_blocks, total_q, free,
+                                             free_blocks.numel(), count, table, seq, cu, slot, pos, left, _ptr(ws), ws_bytes,
+                                             _stream(stream)), w)
 
 
 def dsa_batch_release(done, page_size: int, num_blocks: int, block_table, seq_lens, free_blocks, free_count, ws,
                       ws_bytes: int, stream=None):
     """Gives the blocks of the sequences with done[b] != 0 back to the stack; their seq_lens become 0."""
+    import torch
     w = "dsa_batch_release"
     n = done.numel()
     _shape(seq_lens, (n,), w)
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise DSAError(DSA_ERR_INVALID_ARG, w, f"block_table [{n}, max_blocks] expected")
-    _check(load().dsa_batch_release(
-        _arg(done, _INT, w), n, page_size, block_table.shape[1], num_blocks, _arg(block_table, _INT, w),
-        _arg(seq_lens, _INT, w), _arg(free_blocks, _INT, w), free_blocks.numel(), _arg(free_count, _INT, w), _ptr(ws),
-        ws_bytes, _stream(stream)), w)
+    d, table, seq, free, count = _dense(w, torch.int32, done, block_table, seq_lens, free_blocks, free_count)
+    _check((_lib or load()).dsa_batch_release(d, n, page_size, block_table.shape[1], num_blocks, table, seq, free,
+                                              free_blocks.numel(), count, _ptr(ws), ws_bytes, _stream(stream)), w)
 
 
 def rope_part(x, out, *, weight=None, norm=(0, 0), eps: float = 1e-6, rope=(0, 0), style: str = "pairs", slots=None,
@@ -396,7 +396,7 @@ def rope_part(x, out, *, weight=None, norm=(0, 0), eps: float = 1e-6, rope=(0, 0
                            w_dt=floats[str(weight.dtype)[6:]] if weight is not None else DSA_F32, out_dt=o_dt,
                            rope_style=DSA_ROPE_HALVES if style == "halves" else DSA_ROPE_PAIRS, eps=eps)
     part.rows = T
-    part.device = x.device
+    part.device = x.get_device()
     part.tensors = (x, out, weight, scale, slots)
     return part
 
@@ -404,25 +404,24 @@ def rope_part(x, out, *, weight=None, norm=(0, 0), eps: float = 1e-6, rope=(0, 0
 def dsa_qk_norm_rope(parts, positions, inv_freq, ws, ws_bytes: int, stream=None):
     """RMS norm and position rotation of up to four tensors (rope_part) in one launch: positions [T] int32, inv_freq
     [rope_len / 2] float64."""
+    import torch
     w = "dsa_qk_norm_rope"
     if not 1 <= len(parts) <= 4:
         raise DSAError(DSA_ERR_UNSUPPORTED, w, f"{len(parts)} parts; 1 to 4 are taken")
-    T = parts[0].rows
-    import torch
+    T, cur = parts[0].rows, torch.cuda.current_device()
     for p in parts:
         if p.rows != T:
             raise DSAError(DSA_ERR_INVALID_ARG, w, f"parts of {T} and {p.rows} rows")
-        if p.device.index != torch.cuda.current_device():
-            raise DSAError(DSA_ERR_INVALID_ARG, w, f"a part on {p.device}; the current device is "
-                                                   f"cuda:{torch.cuda.current_device()}")
+        if p.device != cur:
+            raise DSAError(DSA_ERR_INVALID_ARG, w, f"a part on cuda:{p.device}; the current device is cuda:{cur}")
         if inv_freq is not None and p.rope_len and inv_freq.numel() != p.rope_len // 2:
             raise DSAError(DSA_ERR_INVALID_ARG, w, f"{inv_freq.numel()} frequencies for rope_len {p.rope_len}")
     if positions is not None:
         _shape(positions, (T,), w)
+    pos = None if positions is None else _dense(w, torch.int32, positions)[0]
+    freq = None if inv_freq is None else _dense(w, torch.float64, inv_freq)[0]
     arr = (dsa_rope_part_t * len(parts))(*parts)
-    _check(load().dsa_qk_norm_rope(arr, len(parts), None if positions is None else _arg(positions, _INT, w), T,
-                                   None if inv_freq is None else _arg(inv_freq, ("float64",), w), _ptr(ws), ws_bytes,
-                                   _stream(stream)), w)
+    _check((_lib or load()).dsa_qk_norm_rope(arr, len(parts), pos, T, freq, _ptr(ws), ws_bytes, _stream(stream)), w)
 
 
 def dsa_paged_attn_decode(q, dt: int, kv_pool, v_pool, H: int, Dqk: int, Dv: int, softmax_scale: float, pages, kb: int,

@@ -22,6 +22,7 @@ namespace dsa {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxParts = 4;
 constexpr int kRopeAngles = 1024;          // (row, i) pairs whose sine and cosine a CTA keeps
+constexpr int kRopeRows = 64;              // most rows of a CTA
 constexpr int kRopeChunks = 4;             // 8-element pieces a lane works on at a time
 
 struct RopePartDev {
@@ -33,8 +34,8 @@ struct RopePartDev {
   int64_t out_rows;
   int H, D, norm_off, norm_len, rot_off, rot_len;
   float eps;
-  uint8_t x_dt, w_dt, o_dt, halves, x_vec, w_vec, o_vec, wide;   // *_vec: 16-byte accesses allowed; wide: 32 lanes per row
-  int rows_per_cta, heads_per_cta, head_blocks, cta0;
+  uint8_t x_dt, w_dt, o_dt, halves, x_vec, w_vec, o_vec, lanes;   // *_vec: 16-byte accesses allowed; lanes: per row
+  int rows_per_cta, heads_per_cta, head_blocks, cta0, log_gh;
 };
 
 struct RopeArgs {
@@ -117,151 +118,181 @@ __device__ __forceinline__ void rope_store8(void *base, int64_t i, uint8_t dt, b
   }
 }
 
-// G lanes work on a row of a head; a lane holds NR pieces of NI rows at a time (NR * NI = kRopeChunks).
+// G lanes work on a row of a head, NI rows at a time.  A lane holds NR pieces of 8 entries, two and two: the pieces that
+// rotate with one another in the "halves" order, rot_len / 2 entries apart, fall to the same lane, and the pieces outside the
+// rotated range fill up.  So no order of pairs needs another lane, and a warp's loads still cover whole rows.
+// Groups of G lanes stand in a grid of gr rows x gh heads (gh a power of two); a row's sines and cosines stay in registers for
+// all its heads.
+struct RopeTables {
+  float2 turn[kRopeAngles];                // cosine, sine of (row, i)
+  int64_t dst[kRopeRows];                  // output row, -1: skipped
+};
+
+// what the heads of a CTA's rows share; every thread calls it, after its first loads are under way
+__device__ __forceinline__ void rope_tables(const RopeArgs &a, const RopePartDev &p, int row0, int rows, RopeTables &tab) {
+  for (int r = threadIdx.x; r < rows; r += kRopeThreads) {
+    const int t = row0 + r;
+    int64_t d = -1;
+    if (!a.positions || __ldg(a.positions + t) >= 0) {
+      d = p.slots ? __ldg(p.slots + t) : t;
+      if (d >= p.out_rows) {
+        set_status(a.status, kStatusBadIndex);
+        d = -1;
+      }
+    }
+    tab.dst[r] = d;
+  }
+  const int half = p.rot_len / 2;
+  for (int i = threadIdx.x; i < rows * half; i += kRopeThreads) {
+    const int r = i / half;
+    double turns = (double)__ldg(a.positions + row0 + r) * (__ldg(a.inv_freq + (i - r * half)) * 0.15915494309189535);
+    turns -= rint(turns);
+    float s, c;
+    sincospif(2.f * (float)turns, &s, &c);
+    tab.turn[i] = make_float2(c, s);
+  }
+  __syncthreads();
+}
+
 template <int G, int NR>
 __device__ __forceinline__ void rope_rows(const RopeArgs &a, const RopePartDev &p, int row0, int rows, int head0, int heads,
-                                          const float2 *turn, float4 *scratch) {
+                                          RopeTables &tab) {
   constexpr int NI = kRopeChunks / NR, kGroups = kRopeThreads / G;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
-  const int items = rows * heads, D8 = p.D / 8, half = p.rot_len / 2;
-  const int n0 = p.norm_off / 8, n1 = n0 + p.norm_len / 8, r0 = p.rot_off / 8, r1 = r0 + p.rot_len / 8;
-  float4 *mine = scratch + group * (NI * NR * G * 2);      // [item][low, high half of a piece][piece]
-  for (int i0 = 0; i0 < items; i0 += kGroups * NI) {
-    float v[NI][NR][8];
-    int row[NI], head[NI];
-    int64_t dst[NI];
+  const int gh = 1 << p.log_gh, gr = kGroups >> p.log_gh, h_first = group & (gh - 1), r_first = group >> p.log_gh;
+  const int half = p.rot_len / 2;
+  const int n0 = p.norm_off / 8, n1 = n0 + p.norm_len / 8, r0 = p.rot_off / 8, np = half / 8;
+  const int singles = p.D / 8 - 2 * np, sh = (singles + 1) / 2;
+  int piece[NR];                           // -1: none
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int it = i0 + i * kGroups + group;
-      dst[i] = -1;
-      row[i] = it < items ? it / heads : 0;
-      head[i] = head0 + (it < items ? it % heads : 0);
-      if (it < items) {
-        const int t = row0 + row[i];
-        if (!a.positions || __ldg(a.positions + t) >= 0) {
-          dst[i] = p.slots ? __ldg(p.slots + t) : t;
-          if (dst[i] >= p.out_rows) {
-            set_status(a.status, kStatusBadIndex);
-            dst[i] = -1;
-          }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const int c = r * G + lane;
-        if (dst[i] >= 0 && c < D8) {
-          rope_load8(p.x, (int64_t)(row0 + row[i]) * p.x_row + (int64_t)head[i] * p.x_head + 8 * c, p.x_dt, p.x_vec, v[i][r]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[i][r][e] = 0.f;
-        }
-      }
+  for (int r = 0; r < NR; ++r) {
+    const int d = (r / 2) * G + lane;      // the lane's pair of pieces
+    if (d < np) {
+      piece[r] = r0 + d + (r & 1) * np;
+    } else {
+      const int s = d - np + (r & 1) * sh;
+      const bool ok = d - np < sh && s < singles;
+      piece[r] = ok ? (s < r0 ? s : s + 2 * np) : -1;
     }
-    if (p.norm_len) {
+  }
+  bool ready = false;
+  for (int rb = 0; rb < rows; rb += gr) {
+    const int row = rb + r_first;
+    const int64_t x_row = (int64_t)(row0 + row) * p.x_row;
+    int64_t dst = -1;
+    float2 cs[NR / 2][8];
+    for (int hb = 0; hb < heads; hb += gh * NI) {
+      float v[NI][NR][8];
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        float ss = 0.f;
+        const int h = hb + i * gh + h_first;
+        const int64_t at = x_row + (int64_t)(head0 + h) * p.x_head;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          const int c = r * G + lane;
-          if (c >= n0 && c < n1)
+          if (row < rows && h < heads && piece[r] >= 0) {
+            rope_load8(p.x, at + 8 * piece[r], p.x_dt, p.x_vec, v[i][r]);
+          } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(v[i][r][e], v[i][r][e], ss);
-        }
-#pragma unroll
-        for (int o = G / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = 1.f / sqrtf(ss / (float)p.norm_len + p.eps);
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const int c = r * G + lane;
-          if (c >= n0 && c < n1) {
-            float w[8];
-            rope_load8(p.weight, 8 * (c - n0), p.w_dt, p.w_vec, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][r][e] *= inv * w[e];
+            for (int e = 0; e < 8; ++e) v[i][r][e] = 0.f;
           }
         }
       }
-    }
-    if (p.rot_len) {
-      if (p.halves) {                      // partners lie rot_len / 2 entries apart, in another lane's piece
-        __syncwarp();
+      if (!ready) {
+        rope_tables(a, p, row0, rows, tab);
+        ready = true;
+      }
+      if (hb == 0 && row < rows) {
+        dst = tab.dst[row];
+        const float2 *tr = tab.turn + row * half;
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+        for (int r = 0; r < NR / 2; ++r) {
+          const int d = r * G + lane;
+          if (d >= np) continue;
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            const int c = r * G + lane;
-            if (c >= r0 && c < r1) {
-              mine[(2 * i) * (NR * G) + c] = make_float4(v[i][r][0], v[i][r][1], v[i][r][2], v[i][r][3]);
-              mine[(2 * i + 1) * (NR * G) + c] = make_float4(v[i][r][4], v[i][r][5], v[i][r][6], v[i][r][7]);
+          for (int e = 0; e < 8; ++e)      // halves: the pair's 8 angles; pairs: 4 of each piece
+            cs[r][e] = p.halves ? tr[8 * d + e] : tr[4 * d + (e < 4 ? e : e - 4 + half / 2)];
+        }
+      }
+      if (p.norm_len) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          float ss = 0.f;
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            if (piece[r] >= n0 && piece[r] < n1)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) ss = fmaf(v[i][r][e], v[i][r][e], ss);
+#pragma unroll
+          for (int o = G / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float inv = 1.f / sqrtf(ss / (float)p.norm_len + p.eps);
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            if (piece[r] >= n0 && piece[r] < n1) {
+              float w[8];
+              rope_load8(p.weight, 8 * (piece[r] - n0), p.w_dt, p.w_vec, w);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[i][r][e] *= inv * w[e];
             }
-          }
-        __syncwarp();
+        }
       }
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
+      for (int r = 0; r < NR; r += 2) {
+        if ((r / 2) * G + lane >= np) continue;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const int c = r * G + lane;
-          if (c < r0 || c >= r1) continue;
-          const int at = 8 * (c - r0);
-          const float2 *tr = turn + row[i] * half;
+        for (int i = 0; i < NI; ++i) {
           if (p.halves) {
-            const bool low = at < half;
-            const int pc = low ? c + half / 8 : c - half / 8;
-            const float4 f = mine[(2 * i) * (NR * G) + pc], g = mine[(2 * i + 1) * (NR * G) + pc];
-            const float u[8] = {f.x, f.y, f.z, f.w, g.x, g.y, g.z, g.w};
-            const float2 *t2 = tr + (low ? at : at - half);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float2 cs = t2[e];
-              v[i][r][e] = fmaf(v[i][r][e], cs.x, low ? -u[e] * cs.y : u[e] * cs.y);
+              const float2 c = cs[r / 2][e];
+              const float x0 = v[i][r][e], x1 = v[i][r + 1][e];
+              v[i][r][e] = fmaf(x0, c.x, -x1 * c.y);
+              v[i][r + 1][e] = fmaf(x1, c.x, x0 * c.y);
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 cs = tr[at / 2 + e];
-              const float x0 = v[i][r][2 * e], x1 = v[i][r][2 * e + 1];
-              v[i][r][2 * e] = fmaf(x0, cs.x, -x1 * cs.y);
-              v[i][r][2 * e + 1] = fmaf(x1, cs.x, x0 * cs.y);
-            }
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 c = cs[r / 2][4 * q + e];
+                const float x0 = v[i][r + q][2 * e], x1 = v[i][r + q][2 * e + 1];
+                v[i][r + q][2 * e] = fmaf(x0, c.x, -x1 * c.y);
+                v[i][r + q][2 * e + 1] = fmaf(x1, c.x, x0 * c.y);
+              }
           }
         }
-    }
-    if (p.scale) {
+      }
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        float am = 0.f;
+        const int h = hb + i * gh + h_first;
+        const bool live = dst >= 0 && h < heads;
+        if (p.scale) {
+          float am = 0.f;
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(v[i][r][e]));
+#pragma unroll
+          for (int o = G / 2; o; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+          float sc = am / 448.0f;
+          if (sc == 0.f) sc = 1.f;
+          if (live && lane == 0) p.scale[dst * p.H + head0 + h] = sc;
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i][r][e] /= sc;
+        }
+        if (!live) continue;
+        const int64_t at = dst * p.o_row + (int64_t)(head0 + h) * p.o_head;
 #pragma unroll
         for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(v[i][r][e]));
-#pragma unroll
-        for (int o = G / 2; o; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-        float sc = am / 448.0f;
-        if (sc == 0.f) sc = 1.f;
-        if (dst[i] >= 0 && lane == 0) p.scale[dst[i] * p.H + head[i]] = sc;
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[i][r][e] /= sc;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (dst[i] < 0) continue;
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const int c = r * G + lane;
-        if (c < D8) rope_store8(p.out, dst[i] * p.o_row + (int64_t)head[i] * p.o_head + 8 * c, p.o_dt, p.o_vec, v[i][r]);
+          if (piece[r] >= 0) rope_store8(p.out, at + 8 * piece[r], p.o_dt, p.o_vec, v[i][r]);
       }
     }
   }
 }
 
-__global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const __grid_constant__ RopeArgs a) {
-  __shared__ float2 turn[kRopeAngles];
-  __shared__ float4 scratch[kRopeThreads * kRopeChunks * 2];
+__global__ void __launch_bounds__(kRopeThreads, 3) qk_rope_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ RopeTables tab;
   int ip = 0;
   while (ip + 1 < a.nparts && (int)blockIdx.x >= a.part[ip + 1].cta0) ++ip;
   const RopePartDev &p = a.part[ip];
@@ -270,22 +301,10 @@ __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const __grid_cons
   const int rows = min(p.rows_per_cta, a.T - row0), heads = min(p.heads_per_cta, p.H - head0);
   pdl_wait();
   pdl_trigger();
-  if (p.rot_len) {
-    const int half = p.rot_len / 2;
-    for (int i = threadIdx.x; i < rows * half; i += kRopeThreads) {
-      const int t = __ldg(a.positions + row0 + i / half);
-      double turns = (double)t * (__ldg(a.inv_freq + i % half) * 0.15915494309189535);
-      turns -= rint(turns);
-      float s, c;
-      sincospif(2.f * (float)turns, &s, &c);
-      turn[i] = make_float2(c, s);
-    }
-    __syncthreads();
-  }
-  if (p.wide) rope_rows<32, 4>(a, p, row0, rows, head0, heads, turn, scratch);
-  else if (p.D <= 64) rope_rows<8, 1>(a, p, row0, rows, head0, heads, turn, scratch);
-  else if (p.D <= 128) rope_rows<8, 2>(a, p, row0, rows, head0, heads, turn, scratch);
-  else rope_rows<8, 4>(a, p, row0, rows, head0, heads, turn, scratch);
+  if (p.lanes == 4) rope_rows<4, 2>(a, p, row0, rows, head0, heads, tab);
+  else if (p.lanes == 32) rope_rows<32, 4>(a, p, row0, rows, head0, heads, tab);
+  else if (p.D <= 128) rope_rows<8, 2>(a, p, row0, rows, head0, heads, tab);
+  else rope_rows<8, 4>(a, p, row0, rows, head0, heads, tab);
 }
 
 // ------------------------------------------------------------------------------------------------ host
@@ -330,12 +349,16 @@ dsa_status_t qk_rope_launch(const dsa_rope_part_t *parts, int nparts, const int3
     p.x_vec = vec_ok(s.x, p.x_row, s.H > 1 ? p.x_head : 0, dt_size(s.x_dt), 16);
     p.w_vec = (uintptr_t)s.weight % 16 == 0;
     p.o_vec = vec_ok(s.out, p.o_row, s.H > 1 ? p.o_head : 0, dt_size(s.out_dt), s.out_dt == DSA_FP8_E4M3 ? 8 : 16);
-    p.wide = s.D > 256;
-    const int groups = kRopeThreads / (p.wide ? 32 : 8);
-    const int at_once = groups * (p.D <= 64 ? 4 : p.D <= 128 ? 2 : 1);
-    p.heads_per_cta = std::min(p.H, at_once);
+    p.lanes = s.D <= 64 ? 4 : s.D <= 256 ? 8 : 32;
+    const int groups = kRopeThreads / p.lanes, ni = p.D <= 128 ? 2 : 1;      // a CTA holds groups * ni (row, head) pairs at a time
+    p.heads_per_cta = std::min(p.H, groups * ni);
     p.head_blocks = (p.H + p.heads_per_cta - 1) / p.heads_per_cta;
-    p.rows_per_cta = std::max(1, at_once / p.heads_per_cta);
+    p.log_gh = 0;
+    while ((ni << p.log_gh) < p.heads_per_cta) ++p.log_gh;                   // <= log2(groups)
+    // Many rows: several passes per CTA, so that sines and cosines are computed by whole CTAs and not by one warp each.
+    const int gr = groups >> p.log_gh;
+    const int64_t passes = std::min<int64_t>(8, (int64_t)T * p.head_blocks / ((int64_t)148 * 8 * gr));
+    p.rows_per_cta = std::min<int>(kRopeRows, gr * (int)std::max<int64_t>(1, passes));
     if (p.rot_len) p.rows_per_cta = std::min(p.rows_per_cta, kRopeAngles / (p.rot_len / 2));
     p.cta0 = (int)ctas;
     ctas += (int64_t)((T + p.rows_per_cta - 1) / p.rows_per_cta) * p.head_blocks;
