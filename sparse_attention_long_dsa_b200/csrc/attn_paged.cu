@@ -5,9 +5,14 @@
 // Practices for Day-0 Adaptation of Million-Token Context Models on Domestic AI Chips", Four Key Layers 3: the decode
 // unit walks the KV blocks and the partial results are merged by a cross-block reduction).
 //
-// The f32 path: a CTA takes a range of page slots (paged.cuh) for up to 16 heads.  Per tile: keys and values to shared memory as
-// f32, one dot product per (token, head) thread slot, a running maximum and sum per head, then P V with the outputs
-// of a thread in registers.  Tokens past the sequence are never multiplied: what the cache holds there may be anything.
+// The f32 path: a CTA takes a range of page slots (paged.cuh) and its 8 warps take batches of 8 to 32 tokens of it in turn.
+// LT lanes stand over a token's entries, four each, so keys and values go from HBM to registers in whole rows, eight keys and
+// eight values per lane in flight; a lane holds its four entries of every head's q and output.  The partial dot products of
+// HP heads are summed over the LT lanes by halving exchanges (each step halves the values a lane carries: HP - 1 shuffles
+// instead of HP log2(LT)), which leaves each (token, head) in one lane for the softmax; the weights come back through a
+// warp's own shared memory.  Warps are joined at the end of a segment, in their order.  Tokens past the sequence are not
+// loaded: what the cache holds there may be anything.  Bound by HBM up to about 8 heads (8 flop per byte and head), then by
+// the FMA and shuffle issue.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -17,17 +22,15 @@ namespace dsa {
 dsa_status_t paged_mla_launch(const void *q, const void *kv, int H, float softmax_scale, const PagedView &view,
                               const PagedOut &o, int max_workers, cudaStream_t stream, int num_sms, int *workers);
 
-constexpr int kPsThreads = 256;
-constexpr int kPsHeads = 16;                       // most heads
-constexpr int kPsTok = kPage;
-constexpr int kPsOut = kPsHeads * 128 / kPsThreads;  // most outputs of a thread
+constexpr int kPsThreads = 256, kPsWarps = kPsThreads / 32;
+constexpr int kPsSteps = 8;                        // keys (and values) of a lane in flight
 
 struct PsArgs {
   const float *q, *kv, *v;
   PagedView view;
   PagedOut o;
   int H, Dqk, Dv;
-  float scale;
+  float scale_log2;
 };
 
 __device__ __forceinline__ void ps_store(float *p, float v) { *p = v; }
@@ -40,129 +43,220 @@ __device__ __forceinline__ void ps_store4(__nv_bfloat16 *p, const float *v) {
   *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
-__host__ __device__ constexpr int ps_stride(int Dqk) { return (Dqk + 3) / 4 * 4 + 4; }
+// entries d .. d + 3 of a row of D
+__device__ __forceinline__ float4 ps_load4(const float *row, int d, int D, bool vec) {
+  if (vec) return d < D ? __ldg(reinterpret_cast<const float4 *>(row + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  return make_float4(d < D ? __ldg(row + d) : 0.f, d + 1 < D ? __ldg(row + d + 1) : 0.f, d + 2 < D ? __ldg(row + d + 2) : 0.f,
+                     d + 3 < D ? __ldg(row + d + 3) : 0.f);
+}
 
+// z[0..HP) summed over the LT lanes of a token: z[0..HV) of a lane are heads first .. first + HV - 1 afterwards
+template <int LT, int HP>
+__device__ __forceinline__ void ps_reduce(float (&z)[HP], int lane) {
+  int n = HP;
+#pragma unroll
+  for (int bit = LT / 2; bit; bit >>= 1) {
+    if (n > 1) {
+      n /= 2;
+      const bool up = lane & bit;
+#pragma unroll
+      for (int i = 0; i < HP / 2; ++i)
+        if (i < n) {
+          const float send = up ? z[i] : z[i + n], keep = up ? z[i + n] : z[i];
+          z[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+        }
+    } else {
+      z[0] += __shfl_xor_sync(0xffffffffu, z[0], bit);
+    }
+  }
+}
+
+template <int LT, int HP>
+struct PsSmem {
+  static constexpr int kTok = 32 / LT * kPsSteps;  // tokens of a batch
+  float p[kPsWarps][kTok][HP];
+  float alpha[kPsWarps][HP], m[kPsWarps][HP], l[kPsWarps][HP];
+  float o[kPsWarps][HP][4 * LT];
+  uint32_t tmp[33];
+  PagedPlan plan;
+};
+
+template <int LT, int HP>
 __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a, int min_slots) {
+  using Smem = PsSmem<LT, HP>;
+  constexpr int TW = 32 / LT, kTok = Smem::kTok, HV = HP > LT ? HP / LT : 1;
   extern __shared__ float4 sm4[];
-  __shared__ uint32_t s_tmp[33];
-  __shared__ PagedPlan s_plan;
-  __shared__ float s_m[kPsHeads], s_l[kPsHeads], s_alpha[kPsHeads];
+  Smem &S = *reinterpret_cast<Smem *>(sm4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int worker = blockIdx.x, nh = a.H;
-  const int Dqk = a.Dqk, Dv = a.Dv, D4 = (Dqk + 3) / 4, KS = ps_stride(Dqk);
-  float *sq = reinterpret_cast<float *>(sm4);      // [16][4 * D4]
-  float *sk = sq + kPsHeads * 4 * D4;              // [kPsTok][KS]
-  float *sp = sk + kPsTok * KS;                       // [16][kPsTok]
-  float *sv = sp + kPsHeads * kPsTok;              // [64][Dv]
+  const int worker = blockIdx.x, H = a.H, Dqk = a.Dqk, Dv = a.Dv;
+  const bool vk = (Dqk & 3) == 0, vv = (Dv & 3) == 0;
+  const int tg = lane / LT, d0 = 4 * (lane % LT);
+  int first = 0;                                   // this lane's first head after ps_reduce
+  {
+    int n = HP;
+#pragma unroll
+    for (int bit = LT / 2; bit; bit >>= 1)
+      if (n > 1) {
+        n /= 2;
+        if (lane & bit) first += n;
+      }
+  }
   pdl_wait();
   pdl_trigger();
-  plan_pages(a.view, worker, gridDim.x, min_slots, s_tmp, &s_plan);
-  if (tid == 0) a.o.info[worker] = worker_info(a.view, s_plan);
+  plan_pages(a.view, worker, gridDim.x, min_slots, S.tmp, &S.plan);
+  if (tid == 0) a.o.info[worker] = worker_info(a.view, S.plan);
 
-  SegmentWalk walk(s_plan);
+  SegmentWalk walk(S.plan);
   int row, sa, sb, part;
-  while (walk.next(a.view, s_plan, worker, &row, &sa, &sb, &part)) {
+  while (walk.next(a.view, S.plan, worker, &row, &sa, &sb, &part)) {
     const int n = row_tokens(a.view, row, a.o.status);
-    __syncthreads();
-    for (int i = tid; i < kPsHeads * 4 * D4; i += kPsThreads) {
-      const int h = i / (4 * D4), d = i % (4 * D4);
-      sq[i] = h < nh && d < Dqk ? __ldg(a.q + ((int64_t)row * nh + h) * Dqk + d) : 0.f;
+    float4 q[HP], o[HP];
+#pragma unroll
+    for (int h = 0; h < HP; ++h) {
+      q[h] = h < H ? ps_load4(a.q + ((int64_t)row * H + h) * Dqk, d0, Dqk, vk) : make_float4(0.f, 0.f, 0.f, 0.f);
+      q[h].x *= a.scale_log2;
+      q[h].y *= a.scale_log2;
+      q[h].z *= a.scale_log2;
+      q[h].w *= a.scale_log2;
+      o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    if (tid < kPsHeads) {
-      s_m[tid] = -INFINITY;
-      s_l[tid] = 0.f;
+    float m[HV], l[HV];
+#pragma unroll
+    for (int i = 0; i < HV; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
     }
-    float o[kPsOut];
+    constexpr int kPer = kPage / kTok;             // batches of a page
+    for (int u = sa * kPer + warp; u < sb * kPer; u += kPsWarps) {
+      int blk = 0;
+      const int t0 = (u % kPer) * kTok, ntok = slot_tokens(a.view, row, n, u / kPer, &blk, a.o.status) - t0;
+      if (ntok <= 0) continue;                     // the same for the whole warp
+      const float *kr = a.kv + ((int64_t)blk * kPage + t0) * Dqk, *vr = a.v + ((int64_t)blk * kPage + t0) * Dv;
+      float4 k[kPsSteps], v[kPsSteps];
 #pragma unroll
-    for (int j = 0; j < kPsOut; ++j) o[j] = 0.f;
-    for (int sl = sa; sl < sb; ++sl) {
-      int blk;
-      const int ntok = slot_tokens(a.view, row, n, sl, &blk, a.o.status);
-      if (ntok > 0) {
-        const int nt = ntok;
-        const int64_t base = (int64_t)blk * kPage;
-        __syncthreads();
-        for (int i = tid; i < nt * 4 * D4; i += kPsThreads) {
-          const int t = i / (4 * D4), d = i % (4 * D4);
-          sk[t * KS + d] = d < Dqk ? __ldg(a.kv + (base + t) * Dqk + d) : 0.f;
+      for (int s = 0; s < kPsSteps; ++s) {
+        const int t = s * TW + tg;
+        k[s] = v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < ntok) {
+          k[s] = ps_load4(kr + (int64_t)t * Dqk, d0, Dqk, vk);
+          v[s] = ps_load4(vr + (int64_t)t * Dv, d0, Dv, vv);
         }
-        for (int i = tid; i < nt * Dv; i += kPsThreads) sv[i] = __ldg(a.v + base * Dv + i);
-        __syncthreads();
-        for (int i = tid; i < kPsHeads * kPsTok; i += kPsThreads) {
-          const int t = i % kPsTok, h = i / kPsTok;
-          float z = -INFINITY;
-          if (t < nt && h < nh) {
-            const float4 *kr = reinterpret_cast<const float4 *>(sk + t * KS);
-            const float4 *qr = reinterpret_cast<const float4 *>(sq + h * 4 * D4);
-            float acc = 0.f;
-            for (int d = 0; d < D4; ++d) {
-              const float4 k4 = kr[d], q4 = qr[d];
-              acc = fmaf(q4.x, k4.x, acc);
-              acc = fmaf(q4.y, k4.y, acc);
-              acc = fmaf(q4.z, k4.z, acc);
-              acc = fmaf(q4.w, k4.w, acc);
-            }
-            z = acc * a.scale;
-          }
-          sp[h * kPsTok + t] = z;
+      }
+      float z[kPsSteps][HV], mx[HV];
+#pragma unroll
+      for (int i = 0; i < HV; ++i) mx[i] = -INFINITY;
+#pragma unroll
+      for (int s = 0; s < kPsSteps; ++s) {
+        float d[HP];
+#pragma unroll
+        for (int h = 0; h < HP; ++h)
+          d[h] = fmaf(q[h].x, k[s].x, fmaf(q[h].y, k[s].y, fmaf(q[h].z, k[s].z, q[h].w * k[s].w)));
+        ps_reduce<LT, HP>(d, lane);
+#pragma unroll
+        for (int i = 0; i < HV; ++i) {
+          z[s][i] = s * TW + tg < ntok ? d[i] : -INFINITY;
+          mx[i] = fmaxf(mx[i], z[s][i]);
         }
-        __syncthreads();
-        for (int h = warp; h < nh; h += kPsThreads / 32) {
-          float mx = -INFINITY;
-          for (int t = lane; t < kPsTok; t += 32) mx = fmaxf(mx, sp[h * kPsTok + t]);
+      }
+      bool moved = false;
+      float alpha[HV];
 #pragma unroll
-          for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-          const float m_old = s_m[h], m_new = fmaxf(m_old, mx), m_use = m_new == -INFINITY ? 0.f : m_new;
-          float ls = 0.f;
-          for (int t = lane; t < kPsTok; t += 32) {
-            const float e = expf(sp[h * kPsTok + t] - m_use);
-            sp[h * kPsTok + t] = e;
-            ls += e;
-          }
+      for (int i = 0; i < HV; ++i) {
 #pragma unroll
-          for (int off = 16; off; off >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
-          if (lane == 0) {
-            const float al = expf(m_old - m_use);
-            s_alpha[h] = al;
-            s_l[h] = s_l[h] * al + ls;
-            s_m[h] = m_new;
-          }
+        for (int bit = LT; bit < 32; bit <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], bit));
+        const float mn = fmaxf(m[i], mx[i]), use = mn == -INFINITY ? 0.f : mn;
+        alpha[i] = exp2f(m[i] - use);
+        moved |= mn != m[i];
+        m[i] = mn;
+        float ls = 0.f;
+#pragma unroll
+        for (int s = 0; s < kPsSteps; ++s) {
+          const float p = exp2f(z[s][i] - use);
+          S.p[warp][s * TW + tg][first + i] = p;
+          ls += p;
         }
-        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kPsOut; ++j) {
-          const int i = tid + kPsThreads * j;
-          if (i < nh * Dv) {
-            const int h = i / Dv, d = i % Dv;
-            float acc = o[j] * s_alpha[h];
-            for (int t = 0; t < nt; ++t) acc = fmaf(sp[h * kPsTok + t], sv[t * Dv + d], acc);
-            o[j] = acc;
+        for (int bit = LT; bit < 32; bit <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, bit);
+        l[i] = l[i] * alpha[i] + ls;
+        S.alpha[warp][first + i] = alpha[i];
+      }
+      moved = __any_sync(0xffffffffu, moved);
+      __syncwarp();
+      if (moved) {
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+          const float al = S.alpha[warp][h];
+          o[h].x *= al;
+          o[h].y *= al;
+          o[h].z *= al;
+          o[h].w *= al;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < kPsSteps; ++s) {
+        const float4 *pr = reinterpret_cast<const float4 *>(S.p[warp][s * TW + tg]);
+#pragma unroll
+        for (int h4 = 0; h4 < HP / 4; ++h4) {
+          const float4 p4 = pr[h4];
+          const float ph[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float4 &oh = o[4 * h4 + e];
+            oh.x = fmaf(ph[e], v[s].x, oh.x);
+            oh.y = fmaf(ph[e], v[s].y, oh.y);
+            oh.z = fmaf(ph[e], v[s].z, oh.z);
+            oh.w = fmaf(ph[e], v[s].w, oh.w);
           }
         }
       }
+      __syncwarp();
+    }
+    // join the warps, in their order
+#pragma unroll
+    for (int h = 0; h < HP; ++h) {
+#pragma unroll
+      for (int bit = LT; bit < 32; bit <<= 1) {
+        o[h].x += __shfl_xor_sync(0xffffffffu, o[h].x, bit);
+        o[h].y += __shfl_xor_sync(0xffffffffu, o[h].y, bit);
+        o[h].z += __shfl_xor_sync(0xffffffffu, o[h].z, bit);
+        o[h].w += __shfl_xor_sync(0xffffffffu, o[h].w, bit);
+      }
+      if (tg == 0) *reinterpret_cast<float4 *>(&S.o[warp][h][d0]) = o[h];
+    }
+#pragma unroll
+    for (int i = 0; i < HV; ++i) {
+      S.m[warp][first + i] = m[i];
+      S.l[warp][first + i] = l[i];
     }
     __syncthreads();
+    for (int i = tid; i < H * Dv; i += kPsThreads) {
+      const int h = i / Dv, d = i - h * Dv;
+      float M = -INFINITY, L = 0.f, acc = 0.f;
 #pragma unroll
-    for (int j = 0; j < kPsOut; ++j) {
-      const int i = tid + kPsThreads * j;
-      if (i < nh * Dv) {
-        const int h = i / Dv, d = i % Dv;
-        const float l = s_l[h], val = l != 0.f ? o[j] / l : 0.f;
-        if (part < 0) ps_store((float *)a.o.out + ((int64_t)row * nh + h) * Dv + d, val);
-        else a.o.part_o[((int64_t)part * nh + h) * Dv + d] = val;
+      for (int w = 0; w < kPsWarps; ++w) M = fmaxf(M, S.m[w][h]);
+      const float use = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < kPsWarps; ++w) {
+        const float e = exp2f(S.m[w][h] - use);
+        L = fmaf(e, S.l[w][h], L);
+        acc = fmaf(e, S.o[w][h][d], acc);
+      }
+      const float val = L != 0.f ? acc / L : 0.f;
+      if (part < 0) ((float *)a.o.out)[((int64_t)row * H + h) * Dv + d] = val;
+      else a.o.part_o[((int64_t)part * H + h) * Dv + d] = val;
+      if (d == 0) {
+        const float lse = L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+        if (part >= 0) a.o.part_lse[(int64_t)part * H + h] = lse;
+        else if (a.o.lse) a.o.lse[(int64_t)row * H + h] = lse;
       }
     }
-    if (tid < nh) {
-      const float lse = s_l[tid] != 0.f ? s_m[tid] + logf(s_l[tid]) : -INFINITY;
-      if (part >= 0) a.o.part_lse[(int64_t)part * nh + tid] = lse;
-      else if (a.o.lse) a.o.lse[(int64_t)row * nh + tid] = lse;
-    }
+    __syncthreads();
   }
   // rows without a cached token: zeros, and -inf for the log-sum-exp
   for (int r = worker; r < a.view.T; r += gridDim.x) {
     if (row_slots(a.view, r) > 0) continue;
-    for (int i = tid; i < nh * Dv; i += kPsThreads) ps_store((float *)a.o.out + (int64_t)r * nh * Dv + i, 0.f);
-    if (a.o.lse && tid < nh) a.o.lse[(int64_t)r * nh + tid] = -INFINITY;
+    for (int i = tid; i < H * Dv; i += kPsThreads) ((float *)a.o.out)[(int64_t)r * H * Dv + i] = 0.f;
+    if (a.o.lse && tid < H) a.o.lse[(int64_t)r * H + tid] = -INFINITY;
   }
 }
 
@@ -316,6 +410,24 @@ static PagedOut paged_out(void *ws, int H, int Dv, void *out, float *lse) {
   return o;
 }
 
+template <int LT, int HP>
+static dsa_status_t simt_launch(const PsArgs &a, int workers, cudaStream_t stream) {
+  auto *k = paged_simt_kernel<LT, HP>;
+  constexpr size_t smem = sizeof(PsSmem<LT, HP>);
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    set_error("paged_simt_kernel: %s", cudaGetErrorString(cudaGetLastError()));
+    return DSA_ERR_CUDA;
+  }
+  DSA_LAUNCH_PDL("paged_simt_kernel", k, dim3(workers), dim3(kPsThreads), smem, stream, a, 1);
+  return DSA_OK;
+}
+template <int LT>
+static dsa_status_t simt_heads(const PsArgs &a, int workers, cudaStream_t stream) {
+  if (a.H <= 4) return simt_launch<LT, 4>(a, workers, stream);
+  if (a.H <= 8) return simt_launch<LT, 8>(a, workers, stream);
+  return simt_launch<LT, 16>(a, workers, stream);
+}
+
 dsa_status_t paged_attn_launch(const void *q, bool bf16, const void *kv, const void *v, int H, int Dqk, int Dv,
                                float scale, const int32_t *pages, int kb, const dsa_batch_t *b, void *out, float *lse,
                                void *ws, cudaStream_t stream, int num_sms) {
@@ -328,7 +440,7 @@ dsa_status_t paged_attn_launch(const void *q, bool bf16, const void *kv, const v
   a.H = H;
   a.Dqk = Dqk;
   a.Dv = Dv;
-  a.scale = scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
   if (bf16) {
     int workers = 0;
     const dsa_status_t st = paged_mla_launch(q, kv, H, scale, a.view, a.o, paged_max_workers(Dv), stream, num_sms, &workers);
@@ -336,10 +448,13 @@ dsa_status_t paged_attn_launch(const void *q, bool bf16, const void *kv, const v
     return combine_launch<__nv_bfloat16, 4, true>(a.o, workers, b->total_q, H, Dv, stream);
   }
   const int workers = std::min(num_sms, paged_max_workers(Dv));
-  const int D4 = (Dqk + 3) / 4;
-  const size_t smem = 4 * ((size_t)kPsHeads * 4 * D4 + (size_t)kPsTok * ps_stride(Dqk) + kPsHeads * kPsTok + (size_t)kPsTok * Dv);
-  cudaFuncSetAttribute(paged_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  DSA_LAUNCH_PDL("paged_simt_kernel", paged_simt_kernel, dim3(workers), dim3(kPsThreads), smem, stream, a, 2);
+  // the fewest lanes that cover a row with four entries each, the fewest heads in steps of 4, 8, 16
+  const int D = std::max(Dqk, Dv);
+  dsa_status_t st;
+  if (D <= 32) st = simt_heads<8>(a, workers, stream);
+  else if (D <= 64) st = simt_heads<16>(a, workers, stream);
+  else st = simt_heads<32>(a, workers, stream);
+  if (st != DSA_OK) return st;
   if (Dv % 4 == 0) return combine_launch<float, 1, true>(a.o, workers, b->total_q, H, Dv, stream);
   return combine_launch<float, 4, false>(a.o, workers, b->total_q, H, Dv, stream);
 }
