@@ -1,0 +1,101 @@
+"""A paged latent cache whose bookkeeping stays on the device: lengths, block tables and the stack of free blocks.
+
+`PagedCache` holds the three pools of the MLA path (latent rows, FP8 indexer keys, key scales) with the state that
+places tokens in them, and enqueues a serving step on one stream:
+
+    cache.extend(new_lens, total_q)            tables, slots, positions and cu_q of the step (dsa_batch_extend)
+    cache.store(kv, k_idx, ...)                norms and rotation of the step's rows, written to their slots, and of
+                                               its queries (dsa_qk_norm_rope)
+    cache.attend(q, out, ...)                  one-token attention over every cached page or a list of pages
+                                               (dsa_paged_attn_decode); or the sparse path on `cache.batch(...)`
+    cache.release(done)                        finished sequences give their blocks back (dsa_batch_release)
+
+Nothing here computes any part of the method, and no call reads the device: a step that does not fit is refused on the
+device and shows in `check_status`.  Every call may be captured into a graph after its first run outside one.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+
+PAGE = 64
+LATENT, VALUE, ROPE = 576, 512, 64
+IDX_H, IDX_D = 64, 128
+
+
+class PagedCache:
+    """num_seqs sequence slots of at most max_blocks pages each, over num_blocks blocks of 64 tokens.
+
+    kv_pool [num_blocks, 64, 576] bf16, ki_pool [num_blocks, 64, 128] uint8 (e4m3), ks_pool [num_blocks, 64] f32;
+    block_table [num_seqs, max_blocks], seq_lens [num_seqs], free_blocks / free_count: device int32.  heads: query heads
+    of attend(), 1 to 128."""
+
+    def __init__(self, num_seqs: int, num_blocks: int, max_blocks: int, heads: int = 128, device="cuda"):
+        dv = self.device = torch.device(device)
+        self.num_seqs, self.num_blocks, self.max_blocks, self.heads = num_seqs, num_blocks, max_blocks, heads
+        self.kv_pool = torch.zeros((num_blocks, PAGE, LATENT), dtype=torch.bfloat16, device=dv)
+        self.ki_pool = torch.zeros((num_blocks, PAGE, IDX_D), dtype=torch.uint8, device=dv)
+        self.ks_pool = torch.ones((num_blocks, PAGE), dtype=torch.float32, device=dv)
+        self.block_table = torch.zeros((num_seqs, max_blocks), dtype=torch.int32, device=dv)
+        self.seq_lens = torch.zeros(num_seqs, dtype=torch.int32, device=dv)
+        self.cu_q = torch.zeros(num_seqs + 1, dtype=torch.int32, device=dv)
+        self.free_blocks = torch.arange(num_blocks - 1, -1, -1, dtype=torch.int32, device=dv)   # block 0 on top
+        self.free_count = torch.full((1,), num_blocks, dtype=torch.int32, device=dv)
+        self.slots = self.positions = None
+        self._one_each = torch.arange(num_seqs + 1, dtype=torch.int32, device=dv)
+        size = max(B.dsa_batch_workspace_size(B.DSA_OP_BATCH_EXTEND, num_seqs),
+                   B.dsa_workspace_size(B.DSA_OP_PAGED_DECODE, self.decode_batch(), 0, heads, VALUE))
+        self.ws = torch.zeros(size, dtype=torch.uint8, device=dv)
+
+    def extend(self, new_lens, total_q: int, stream=None):
+        """A step of new_lens [num_seqs] tokens (device int32), total_q of them or fewer: grows the tables and lengths and
+        fills cu_q, slots [total_q] and positions [total_q]."""
+        if self.slots is None or self.slots.numel() != total_q:
+            self.slots = torch.empty(total_q, dtype=torch.int64, device=self.device)
+            self.positions = torch.empty(total_q, dtype=torch.int32, device=self.device)
+        B.dsa_batch_extend(self.seq_lens, new_lens, PAGE, self.num_blocks, total_q, self.free_blocks, self.free_count,
+                           self.block_table, self.seq_lens, self.cu_q, self.slots, self.positions, self.free_count, self.ws,
+                           self.ws.numel(), stream)
+
+    def release(self, done, stream=None):
+        """Sequences with done[b] != 0 give their blocks back and become empty."""
+        B.dsa_batch_release(done, PAGE, self.num_blocks, self.block_table, self.seq_lens, self.free_blocks, self.free_count,
+                            self.ws, self.ws.numel(), stream)
+
+    def store(self, kv, kv_weight, inv_freq, k_idx=None, k_idx_weight=None, q_rot=None, q=None, q_idx=None, q_idx_out=None,
+              eps: float = 1e-6, stream=None):
+        """The step's rows, total_q of them: kv [total_q, 576] (512 normed by kv_weight, 64 rotated in pairs) and k_idx
+        [total_q, 128] (normed by k_idx_weight, its first 64 rotated in halves, e4m3 with a scale) go to their slots; q_rot
+        [total_q, heads, 64] is rotated into q[:, :, 512:] and q_idx [total_q, 64, 128] (first 64 rotated in halves) into
+        q_idx_out as e4m3 codes.  Up to three of them may be left out."""
+        parts = [B.rope_part(kv, self.kv_pool.view(-1, LATENT), weight=kv_weight, norm=(0, VALUE), eps=eps, rope=(VALUE, ROPE),
+                             slots=self.slots)]
+        if k_idx is not None:
+            parts.append(B.rope_part(k_idx, self.ki_pool.view(-1, IDX_D), weight=k_idx_weight, norm=(0, IDX_D), eps=eps,
+                                     rope=(0, ROPE), style="halves", slots=self.slots, scale=self.ks_pool.view(-1)))
+        if q_rot is not None:
+            parts.append(B.rope_part(q_rot, q[:, :, VALUE:], rope=(0, ROPE)))
+        if q_idx is not None:
+            parts.append(B.rope_part(q_idx, q_idx_out, rope=(0, ROPE), style="halves"))
+        B.dsa_qk_norm_rope(parts, self.positions, inv_freq, self.ws, self.ws.numel(), stream)
+
+    def batch(self, total_q: int, max_q_per_seq: int, max_seq_len: int):
+        """The step's batch descriptor for the other calls (upper bounds as in make_batch)."""
+        return B.make_batch(self.block_table, self.seq_lens, self.cu_q, num_blocks=self.num_blocks, page_size=PAGE,
+                            total_q=total_q, max_q_per_seq=max_q_per_seq, max_seq_len=max_seq_len)
+
+    def decode_batch(self):
+        """One row per sequence slot, empty ones included."""
+        return B.make_batch(self.block_table, self.seq_lens, self._one_each, num_blocks=self.num_blocks, page_size=PAGE,
+                            total_q=self.num_seqs, max_q_per_seq=1, max_seq_len=self.max_blocks * PAGE)
+
+    def attend(self, q, out, softmax_scale: float, pages=None, lse=None, stream=None):
+        """q [num_seqs, heads, 576] over every cached token of its sequence, or over the tokens of the pages in pages
+        [num_seqs, kb] (int32, -1: none); out [num_seqs, heads, 512].  Empty slots give zeros."""
+        kb = 0 if pages is None else pages.shape[1]
+        B.dsa_paged_attn_decode(q, B.DSA_BF16, self.kv_pool, None, self.heads, LATENT, VALUE, softmax_scale, pages, kb,
+                                self.decode_batch(), out, lse, self.ws, self.ws.numel(), stream)
+
+    def check_status(self, stream=None):
+        B.dsa_read_device_status(self.ws, stream)

@@ -150,11 +150,10 @@ class DeviceBatch:
         B.dsa_gather_positions(self._cand_sel, k, self.cand, m, T, self.idx_reuse, stream)
         return self.idx_reuse
 
-    def block_select(self, kb, stream=None):
-        """Block-granular selection from the current scores: page scores, the kb best pages per row (the
-        usual top-k on a batch of the rows' page lists) and their token positions.  Returns the index
-        array [total_q, kb * page_size] for attention(idx=..., k=kb * page_size); the page scores, page
-        counts and kept pages stay in blk_scores, blk_lens and blk_idx."""
+    def block_pages(self, kb, stream=None):
+        """The kb best pages per row from the current scores: page scores, then the usual top-k on a batch of the rows'
+        page lists.  Returns blk_idx [total_q, kb] (ascending, -1 padding); the page scores and page counts stay in
+        blk_scores and blk_lens."""
         wl, dv, T, P = self.wl, self.device, self.wl.total_q, self.wl.page_size
         max_pages = (wl.max_seq_len + P - 1) // P
         if getattr(self, "_blk_kb", None) != kb:
@@ -178,8 +177,26 @@ class DeviceBatch:
         B.dsa_block_scores(self.scores, self.ld, self.batch, self.blk_scores, self.ld_blk, self.blk_lens, stream)
         B.dsa_topk(self.blk_scores, self.ld_blk, self.blk_batch, kb, self.blk_idx, self._blk_ws, self._blk_ws_bytes,
                    stream)
+        return self.blk_idx
+
+    def block_select(self, kb, stream=None):
+        """Block-granular selection from the current scores: block_pages and their token positions.  Returns the index
+        array [total_q, kb * page_size] for attention(idx=..., k=kb * page_size); the page scores, page
+        counts and kept pages stay in blk_scores, blk_lens and blk_idx."""
+        self.block_pages(kb, stream)
         B.dsa_expand_blocks(self.blk_idx, kb, self.batch, self.idx_blk, stream)
         return self.idx_blk
+
+    def paged_attention(self, pages=None, stream=None):
+        """Attention of a decode batch over every cached page, or over the pages in pages [total_q, kb] (such as
+        block_pages gives), without expanding them to token positions."""
+        wl = self.wl
+        kb = 0 if pages is None else pages.shape[1]
+        need = B.dsa_workspace_size(B.DSA_OP_PAGED_DECODE, self.batch, kb, wl.H, wl.Dv)
+        if getattr(self, "_paged_ws", None) is None:
+            self._paged_ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        B.dsa_paged_attn_decode(self.q, self.dt, self.kv_pool, self.v_pool, wl.H, wl.Dqk, wl.Dv, wl.softmax_scale, pages, kb,
+                                self.batch, self.out, self.lse, self._paged_ws, need, stream)
 
     # Batches where the fused scores + selection call is the faster form of the first two steps (measured on
     # one B200): many rows longer than one CTA's shared-memory slice of the plain top-k (the mixed batch's

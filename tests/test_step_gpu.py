@@ -17,7 +17,11 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from sparse_attention_long_dsa_b200 import binding as B
+from sparse_attention_long_dsa_b200 import workloads as W
+from sparse_attention_long_dsa_b200.paged_cache import PagedCache
+from sparse_attention_long_dsa_b200.pipeline import DeviceBatch
 
 pytestmark = pytest.mark.gpu
 
@@ -685,3 +689,126 @@ def test_prompt_and_decode_steps_through_the_three_calls(heads):
         got = pool.view(-1, 576)[torch.tensor(c.table_h[b][tok // 64] * 64 + tok % 64, device=DEV)]
         ref, pre = _rope_ref(inputs[b][:, None], tok, w.double().cpu().numpy(), (0, 512), float(np.float32(1e-6)), (512, 64), "pairs")
         _check(got, ref[:, 0], pre[:, 0], "bf16")
+
+
+def _view(cache, heads):
+    """A _Cache over a PagedCache's state, for its check."""
+    c = _Cache.__new__(_Cache)
+    c.table, c.lens, c.blocks = cache.block_table, cache.seq_lens, cache.num_blocks
+    c.table_h, c.lens_h = cache.block_table.cpu().numpy(), cache.seq_lens.cpu().tolist()
+    c.kv, c.v, c.dqk, c.dv, c.dt, c.torch_dt = cache.kv_pool, None, 576, 512, B.DSA_BF16, torch.bfloat16
+    return c
+
+
+def test_paged_cache_sparse_and_paged_attention_agree():
+    """A prompt and a decode step in a PagedCache; the sparse path's calls on the same cache (scores, every position
+    selected) and the paged attention give the same result, each within its rounding of the 64-bit one."""
+    rng = np.random.default_rng(77)
+    n, heads = 4, 128
+    cache = PagedCache(n, 60, 12, heads)
+    f = lambda *s: torch.tensor(rng.standard_normal(s), device=DEV).bfloat16()        # noqa: E731
+    w_kv, w_ki, freq = f(512).abs() + 0.5, f(128).abs() + 0.5, torch.tensor(_freq(64), device=DEV)
+    for add in ([70, 300, 1, 0], [1, 1, 1, 0]):
+        t = sum(add) + 2
+        cache.extend(_i32(add), t)
+        q_idx_out = torch.zeros((t, 64, 128), dtype=torch.uint8, device=DEV)
+        q = torch.zeros((t, heads, 576), dtype=torch.bfloat16, device=DEV)
+        q[:, :, :512] = f(t, heads, 512)
+        cache.store(f(t, 576), w_kv, freq, k_idx=f(t, 128), k_idx_weight=w_ki, q_rot=f(t, heads, 64), q=q, q_idx=f(t, 64, 128),
+                    q_idx_out=q_idx_out)
+        cache.check_status()
+    q4 = torch.zeros((n, heads, 576), dtype=torch.bfloat16, device=DEV)
+    q4[:3] = q[:3]
+    out, lse = torch.empty((n, heads, 512), dtype=torch.bfloat16, device=DEV), torch.empty((n, heads), device=DEV)
+    cache.attend(q4, out, 0.07, lse=lse)
+    cache.check_status()
+    c = _view(cache, heads)
+    assert c.lens_h == [71, 301, 2, 0]
+    c.check(q4, 0.07, out, lse)
+    # the sparse path over the same cache: three sequences, 512 candidates at most, all of them selected
+    batch = B.make_batch(cache.block_table[:3], cache.seq_lens[:3], cache.cu_q[:4], num_blocks=60, page_size=64, total_q=3,
+                         max_q_per_seq=1, max_seq_len=301)
+    scores = torch.zeros((3, 304), device=DEV)
+    idx = torch.zeros((3, 512), dtype=torch.int32, device=DEV)
+    size = max(B.dsa_workspace_size(B.DSA_OP_INDEXER_TOPK, batch, 512), B.dsa_workspace_size(B.DSA_OP_ATTN_DECODE, batch, 512, 128, 512))
+    ws = _zeros_ws(size)
+    wts = torch.rand((3, 64), device=DEV)
+    B.dsa_indexer_topk(q_idx_out[:3].contiguous(), B.DSA_FP8_E4M3, wts, cache.ki_pool, B.DSA_FP8_E4M3, cache.ks_pool, 64, 128,
+                       batch, 512, scores, 304, idx, ws, size)
+    o2, l2 = torch.empty((3, heads, 512), dtype=torch.bfloat16, device=DEV), torch.empty((3, heads), device=DEV)
+    B.dsa_sparse_attn_decode(q4[:3], B.DSA_BF16, cache.kv_pool, None, heads, 576, 512, 0.07, idx, 512, batch, o2, l2, ws, size)
+    B.dsa_read_device_status(ws)
+    for b, m in enumerate((71, 301, 2)):
+        assert idx[b].tolist() == list(range(m)) + [-1] * (512 - m)
+    full = torch.zeros_like(out)
+    full[:3] = o2
+    lfull = torch.full_like(lse, -float("inf"))
+    lfull[:3] = l2
+    c.check(q4, 0.07, full, lfull)
+
+
+def test_a_captured_step_replays_as_the_cache_grows():
+    """Tables, stores and attention of one decode step in a graph; replays advance the same state, across page borders,
+    with slots that are empty and slots that pause."""
+    n, heads = 3, 16
+    cache = PagedCache(n, 12, 4, heads)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    new = _i32([1, 1, 0])
+    kv = torch.zeros((n, 576), dtype=torch.bfloat16, device=DEV)
+    q = torch.randn((n, heads, 576), generator=g, device=DEV).bfloat16()
+    w, freq = torch.ones(512, device=DEV), torch.tensor(_freq(64), device=DEV)
+    out, lse = torch.empty((n, heads, 512), dtype=torch.bfloat16, device=DEV), torch.empty((n, heads), device=DEV)
+
+    def step():
+        cache.extend(new, n)
+        cache.store(kv, w, freq)
+        cache.attend(q, out, 0.07, lse=lse)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    want = np.array([1, 1, 0])
+    for i in range(150):
+        add = [1, int(i % 3 != 0), int(i >= 70)]
+        new.copy_(_i32(add))
+        kv.copy_(torch.randn((n, 576), generator=g, device=DEV))
+        graph.replay()
+        want += add
+        if i in (0, 61, 62, 63, 80, 127, 149):
+            cache.check_status()
+            assert cache.seq_lens.tolist() == want.tolist()
+            _view(cache, heads).check(q, 0.07, out, lse)
+
+
+@pytest.mark.parametrize("kind", ["mla", "f32"])
+def test_device_batch_paged_attention(kind):
+    """The batch's own paged attention: over every page, and over the pages that its block selection keeps, against the
+    attention over their token positions."""
+    if kind == "mla":
+        wl = W.make_workload("paged", kind="mla", seed=31, seq_lens=[700, 64, 65, 1500, 1], q_lens=[1] * 5, topk=128)
+    else:
+        wl = W.make_workload("paged32", kind="f32", seed=32, seq_lens=[700, 64, 65, 1500, 1], q_lens=[1] * 5, topk=128, H=4,
+                             Dqk=64, Dv=64, Hi=2, Di=32)
+    db = DeviceBatch(wl)
+    db.indexer()
+    tol = 2e-2 if kind == "mla" else 1e-5
+    for kb in (None, 3):
+        if kb is None:
+            db.paged_attention()
+            idx = np.full((5, 1536), -1)
+            for b, m in enumerate(wl.seq_lens):
+                idx[b, :m] = np.arange(m)
+        else:
+            idx = db.block_select(kb).cpu().numpy()
+            db.paged_attention(db.block_pages(kb))
+        torch.cuda.synchronize()
+        out, lse = db.out.float().cpu().numpy(), db.lse.cpu().numpy()
+        for b in range(5):
+            ref, ref_lse = oracle.sparse_attention_row(wl, b, idx[b])
+            assert np.abs(out[b] - ref).max() <= tol and np.abs(lse[b] - ref_lse).max() <= (1e-3 if kind == "mla" else 1e-5)
