@@ -262,17 +262,17 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a, 
 
 // ------------------------------------------------------------------------------------------------ join
 // out[row, h, :] = sum_w exp(lse_w - lse) o_w,  lse = log sum_w exp(lse_w)  over the workers w that hold a part of the row.
-// At most min(T, workers) rows are split; CTA x finds the x-th of them in info, a warp takes a head (kGroup = 1) or every
+// At most min(T, workers) rows are split, and CTA x finds the x-th of them in info; a warp takes a head (kGroup = 1) or every
 // kGroup-th part of one (the sums of the kGroup warps are added in a fixed order).  A lane holds kN pieces of the row (four
-// values each where Dv % 4 == 0, else single ones).  Bound by latency: three dependent loads, so it is the number of warps in
-// flight that counts.  Few rows have many parts each: kGroup = 8 up to 1,184 (row, head) pairs, one CTA of 8 warps per head
-// (a 1M-token row, 74 parts of 128 heads: 8 us, 90 us with one warp per head and part after part); more rows have few parts:
-// a warp per head (the 32-row decode batch, 3.3 parts each: 6 us, 28 us with 16 warps per head).
-constexpr int kPcThreads = 256, kPcWarps = kPcThreads / 32, kPcMaxWorkers = 160;
+// values each where Dv % 4 == 0, else single ones).  Bound by latency, so it is the number of warps in flight that counts.
+// Few rows have many parts each: kGroup = 8 up to 1,184 (row, head) pairs, one CTA of 8 warps per head (a 1M-token row, 74
+// parts of 128 heads: 8 us, 90 us with part after part); more rows have few parts: a warp per head (the 32-row decode batch,
+// 3.3 parts each, 28 us with 16 warps per head).
+constexpr int kPcThreads = 256, kPcWarps = kPcThreads / 32, kPcMaxParts = 160;
 
 template <typename T, int kGroup, int kN, bool kVec>
 __global__ void __launch_bounds__(kPcThreads) paged_combine_kernel(const PagedOut o, int workers, int H, int Dv) {
-  constexpr int kLane = kVec ? 4 : 1, kBlocks = kPcMaxWorkers / 32;
+  constexpr int kLane = kVec ? 4 : 1, kBlocks = kPcMaxParts / 32;
   __shared__ float s_acc[kGroup > 1 ? kPcWarps : 1][kN * kLane * 32];
   pdl_wait();
   pdl_trigger();
@@ -305,6 +305,26 @@ __global__ void __launch_bounds__(kPcThreads) paged_combine_kernel(const PagedOu
   if (live) {
     // part s: the first worker's odd slot, then the even slots of the workers after it
     auto slot = [&](int s) { return (int64_t)(2 * (first + s) + (s == 0 ? 1 : 0)) * H + h; };
+    auto load = [&](int s, float (&v)[kN * kLane]) {
+      const float *p = o.part_o + slot(s) * Dv;
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const int d = (32 * k + lane) * kLane;
+        if (kVec) {
+          const float4 f = d < Dv ? __ldg(reinterpret_cast<const float4 *>(p + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[kLane * k] = f.x;
+          v[kLane * k + kLane / 4] = f.y;
+          v[kLane * k + kLane / 2] = f.z;
+          v[kLane * k + kLane - 1] = f.w;
+        } else {
+          v[k] = d < Dv ? __ldg(p + d) : 0.f;
+        }
+      }
+    };
+    // the first parts' values are on their way while the weights are worked out
+    float v0[kN * kLane], v1[kN * kLane];
+    if (sub < n) load(sub, v0);
+    if (sub + kGroup < n) load(sub + kGroup, v1);
     float w[kBlocks], mx = -INFINITY, tot = 0.f;
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
@@ -326,25 +346,15 @@ __global__ void __launch_bounds__(kPcThreads) paged_combine_kernel(const PagedOu
     for (int i = 0; i < kBlocks; ++i) {
       if (32 * i >= n) break;
       const int top = min(32, n - 32 * i);
-#pragma unroll 2
       for (int l = sub; l < top; l += kGroup) {    // 32 is a multiple of kGroup
+        const int s = 32 * i + l;
         const float ws = __shfl_sync(0xffffffffu, w[i], l) * inv;
-        const float *p = o.part_o + slot(32 * i + l) * Dv;
 #pragma unroll
-        for (int k = 0; k < kN; ++k) {
-          const int d = (32 * k + lane) * kLane;
-          if (d < Dv) {
-            if (kVec) {
-              const float4 v = __ldg(reinterpret_cast<const float4 *>(p + d));
-              acc[kLane * k] = fmaf(ws, v.x, acc[kLane * k]);
-              acc[kLane * k + kLane / 4] = fmaf(ws, v.y, acc[kLane * k + kLane / 4]);
-              acc[kLane * k + kLane / 2] = fmaf(ws, v.z, acc[kLane * k + kLane / 2]);
-              acc[kLane * k + kLane - 1] = fmaf(ws, v.w, acc[kLane * k + kLane - 1]);
-            } else {
-              acc[k] = fmaf(ws, __ldg(p + d), acc[k]);
-            }
-          }
+        for (int k = 0; k < kN * kLane; ++k) {
+          acc[k] = fmaf(ws, v0[k], acc[k]);
+          v0[k] = v1[k];
         }
+        if (s + 2 * kGroup < n) load(s + 2 * kGroup, v1);
       }
     }
   }

@@ -39,7 +39,7 @@ constexpr int kPtWarpKeys = 8, kPtWarpQK = 9, kPtWarpPV = 10, kPtWarpValues = 11
 constexpr uint32_t kPtBlk = kPtHalf * 128;         // one 64-entry block of a CTA's 32 tokens: 4 KB
 constexpr uint32_t kPtBuf = 9 * kPtBlk;
 constexpr uint32_t kPtQ = 9 * 8192;
-constexpr uint32_t kPtP = 8192;                    // [64 heads][64 tokens] bf16; epilogue staging
+constexpr uint32_t kPtP = 4096;                    // half of P: [64 heads][32 tokens] bf16, 64-byte swizzle
 constexpr uint32_t kPtTmemO = 0, kPtTmemS = 256;
 constexpr float kPtRescale = 8.0f;
 constexpr int kPtFirst = 1, kPtLast = 2, kPtEmpty = 4, kPtEnd = 8;
@@ -50,8 +50,7 @@ struct PtSmem {
   uint64_t v_full[kPtNBuf];         // rank 0: bytes of both CTAs' peer values
   uint64_t q_full, q_empty;
   uint64_t s_full[kPtNBuf];
-  uint64_t p_full;
-  uint64_t pv_done[2];              // by page parity: a group waits for every phase of the other group's barrier
+  uint64_t p_full[2], pv_done[2];   // by page parity
   uint64_t o_empty, drain[2];
   uint64_t ent_full[kPtRing], ent_empty[kPtRing];
   uint32_t tmem_base;
@@ -118,6 +117,16 @@ __device__ __forceinline__ bool pt_any(int g, bool x) {
       : "memory");
   return r != 0;
 }
+// K-major operand in rows of 64 bytes, 8-row atoms of 512 bytes, 64-byte swizzle
+__device__ __forceinline__ uint64_t pt_desc_sw64(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)1u << 16;
+  d |= (uint64_t)(512u >> 4) << 32;
+  d |= (uint64_t)1u << 46;                              // descriptor version (sm_100)
+  d |= (uint64_t)4u << 61;                              // layout: 64-byte swizzle
+  return d;
+}
 __device__ __forceinline__ bool pt_elect() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
@@ -175,8 +184,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sQ = smem;                              // [9 blocks][64 heads][128 B]
   uint8_t *sBuf = sQ + kPtQ;                       // 4 x [9 blocks][32 tokens][128 B]
-  uint8_t *sP = sBuf + kPtNBuf * kPtBuf;
-  PtSmem *S = (PtSmem *)(sP + kPtP);
+  uint8_t *sP = sBuf + kPtNBuf * kPtBuf;           // second halves of two pages' P; epilogue staging
+  PtSmem *S = (PtSmem *)(sP + 2 * kPtP);
 
   const uint32_t rank = tc::cluster_ctarank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -189,9 +198,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       tc::mbar_init(tc::smem_u32(&S->v_full[i]), 1);
       tc::mbar_init(tc::smem_u32(&S->s_full[i]), 1);
     }
-    tc::mbar_init(tc::smem_u32(&S->p_full), 8);
     tc::mbar_init(tc::smem_u32(&S->st_free), 4);
     for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tc::smem_u32(&S->p_full[i]), 8);
       tc::mbar_init(tc::smem_u32(&S->pv_done[i]), 1);
       tc::mbar_init(tc::smem_u32(&S->dec[i]), 4);
       tc::mbar_init(tc::smem_u32(&S->l_ready[i]), 4);
@@ -241,7 +250,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
 
   if (warp == kPtWarpKeys) {
     // ====================================================================== pages, keys and q
-    if (lane == 0 && rank == 0) a.o.info[pair] = worker_info(a.view, S->plan);
     const int oob = a.view.num_blocks * kPage;             // a row outside the map: zero-filled
     const uint32_t buf_full_r0 = tc::map_to_rank(tc::smem_u32(&S->buf_full[0]), 0);
     const uint32_t q_full_r0 = tc::map_to_rank(tc::smem_u32(&S->q_full), 0);
@@ -305,6 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       if (ok) ok = h_ntok ? page(h_phys, h_ntok, row, flags | kPtLast | tag) : publish(0, 0, row, kPtEmpty | tag);
     }
     if (ok) publish(0, 0, 0, kPtEnd);
+    if (lane == 0 && rank == 0) a.o.info[pair] = worker_info(a.view, S->plan);
   } else if (warp == kPtWarpValues) {
     // ====================================================================== the peer's values
     const int oob = a.view.num_blocks * kPage;
@@ -362,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         }
       } else {
         constexpr uint32_t idesc = tc::make_idesc(1, 1, 128, 256, false, true);
-        const uint64_t p_desc = tc::desc_sw128(tc::smem_u32(sP), 1024);
+        const uint64_t p0_desc = pt_desc_sw64(tc::smem_u32(sBuf + 8 * kPtBlk)), p1_desc = pt_desc_sw64(tc::smem_u32(sP));
         const uint64_t v_desc = tc::desc_sw128_lbo(tc::smem_u32(sBuf), kPtBlk, 1024);
         while (next_entry(ec, &e)) {
           const int info = __shfl_sync(0xffffffffu, e.w, 0);
@@ -375,16 +384,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
             ++segs;
           }
           if (!pt_wait(tc::smem_u32(&S->v_full[b]), (c / kPtNBuf) & 1u, abort, status)) break;
-          if (!pt_wait_cl(tc::smem_u32(&S->p_full), c & 1u, abort, status)) break;
+          if (!pt_wait_cl(tc::smem_u32(&S->p_full[c & 1u]), (c >> 1) & 1u, abort, status)) break;
           tc::fence_after_sync();
           const uint64_t vb = v_desc + ((b * kPtBuf) >> 4);
+          const uint64_t p0 = p0_desc + ((b * kPtBuf) >> 4), p1 = p1_desc + (((c & 1u) * kPtP) >> 4);
           if (pt_elect()) {
-            // K steps of 16 tokens: token half (4 blocks apart) x two steps of 16 rows
+            // K steps of 16 tokens: token half (4 blocks apart) x two steps of 16 rows; both value halves share a step of P
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                pt_mma_pair(tm + kPtTmemO + 128 * p, p_desc + 2 * k,
+              for (int p = 0; p < 2; ++p)
+                pt_mma_pair(tm + kPtTmemO + 128 * p, (k < 2 ? p0 : p1) + 2 * (k & 1),
                             vb + ((2 * p * kPtBlk + (k >> 1) * 4 * kPtBlk + (k & 1) * 16 * 128) >> 4), idesc, k > 0 || !first);
           }
           __syncwarp();
@@ -407,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     const int h = L & 63, half = L >> 6;
     const int head = 64 * (int)rank + h;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t p_full_r0 = tc::map_to_rank(tc::smem_u32(&S->p_full), 0);
+    const uint32_t p_full_r0 = tc::map_to_rank(tc::smem_u32(&S->p_full[0]), 0) + 8 * g;
     const uint32_t o_empty_r0 = tc::map_to_rank(tc::smem_u32(&S->o_empty), 0);
     __nv_bfloat16 *out = (__nv_bfloat16 *)a.o.out;
     float m_run = -INFINITY, l_run = 0.f;          // this thread's tokens of the segment: reference, sum of weights
@@ -466,7 +476,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         // TMEM accesses are warp-collective: every row of the warp is brought to its new reference.  P V of the previous
         // page must have finished before O is touched.
         if (!first && __any_sync(0xffffffffu, m_new > m_run)) {
-          ok = pt_wait(tc::smem_u32(&S->pv_done[(c - 1) & 1u]), ((c - 1) >> 1) & 1u, abort, status);
+          // (P V of page c - 2 first: it shows that page c - 3's has run too, so that the phase asked for is the next one)
+          if (c >= 2) pt_wait(tc::smem_u32(&S->pv_done[g]), ((c - 2) >> 1) & 1u, abort, status);
+          ok = pt_wait(tc::smem_u32(&S->pv_done[g ^ 1]), ((c - 1) >> 1) & 1u, abort, status);
           tc::fence_after_sync();
           const float alpha = m_new > m_run ? tc::ex2(m_run - m_new) : 1.f;
           if (ok) {
@@ -516,28 +528,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         pw[i] = *reinterpret_cast<const uint32_t *>(&pb);
       }
       l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-      // the P buffer was last read by P V of the page before, or by the epilogue of the segment before
-      if (c > 0) ok = pt_wait(tc::smem_u32(&S->pv_done[(c - 1) & 1u]), ((c - 1) >> 1) & 1u, abort, status) && ok;
+      // Tokens 0-31 go where the page's last key block was (QK^T has read it), tokens 32-63 to one of two buffers, last read by
+      // P V of page c - 2 or by the epilogue of the segment before
+      if (c >= 2) ok = pt_wait(tc::smem_u32(&S->pv_done[g]), ((c - 2) >> 1) & 1u, abort, status) && ok;
       if (first && seg > 0) ok = pt_wait(tc::smem_u32(&S->st_free), (seg - 1) & 1u, abort, status) && ok;
       if (ok) {
-        uint8_t *pbuf = sP + h * 128;
+        uint8_t *pbuf = (half == 0 ? sBuf + (c % kPtNBuf) * kPtBuf + 8 * kPtBlk : sP + g * kPtP) + h * 64;
 #pragma unroll
         for (int q8 = 0; q8 < 4; ++q8)
-          *reinterpret_cast<uint4 *>(pbuf + (((4 * half + q8) ^ (h & 7)) << 4)) =
+          *reinterpret_cast<uint4 *>(pbuf + ((q8 ^ ((h >> 1) & 3)) << 4)) =
               make_uint4(pw[4 * q8], pw[4 * q8 + 1], pw[4 * q8 + 2], pw[4 * q8 + 3]);
       }
       tc::fence_proxy_async();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) {
-        if (rank == 0) tc::mbar_arrive(tc::smem_u32(&S->p_full));
+        if (rank == 0) tc::mbar_arrive(tc::smem_u32(&S->p_full[g]));
         else tc::mbar_arrive_remote(p_full_r0);
       }
       ++c;
       if (!last) continue;
 
       // ---- epilogue: wait for the last P V, add up the sums, normalise and store
-      ok = pt_wait(tc::smem_u32(&S->pv_done[(c - 1) & 1u]), ((c - 1) >> 1) & 1u, abort, status) && ok;
+      ok = pt_wait(tc::smem_u32(&S->pv_done[g]), ((c - 1) >> 1) & 1u, abort, status) && ok;
       ok = pt_wait(tc::smem_u32(&S->l_ready[seg & 1u]), (seg >> 1) & 1u, abort, status) && ok;
       tc::fence_after_sync();
       S->x[g][L] = l_run + S->lp[seg & 1u][L];
@@ -656,7 +669,7 @@ dsa_status_t paged_mla_launch(const void *q, const void *kv, int H, float softma
     set_error("paged attention: cuTensorMapEncodeTiled failed");
     return DSA_ERR_CUDA;
   }
-  constexpr size_t smem = kPtQ + kPtNBuf * kPtBuf + kPtP + sizeof(PtSmem);
+  constexpr size_t smem = kPtQ + kPtNBuf * kPtBuf + 2 * kPtP + sizeof(PtSmem);
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   // as many CTA pairs as can be resident at once, found once per device (threads that race on the first call
   // compute the same number)

@@ -98,21 +98,18 @@ __device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int w
     p->np = np;
     p->start = start;
     p->end = end;
-    p->row = 0;
-    p->page = 0;
   }
-  __syncthreads();
-  if (start < end && start >= before && start < before + mine) {
+  if (start < end && start >= before && start < before + mine) {     // one thread; no worker without slots reads row and page
     uint32_t at = before;
-    for (int r = r0; r < r1; ++r) {
-      const uint32_t n = (uint32_t)row_slots(v, r);
-      if (start < at + n) {
-        p->row = r;
-        p->page = (int)(start - at);
-        break;
+    int r = r0;
+    if (per > 1)
+      for (;; ++r) {
+        const uint32_t n = (uint32_t)row_slots(v, r);
+        if (start < at + n) break;
+        at += n;
       }
-      at += n;
-    }
+    p->row = r;
+    p->page = (int)(start - at);
   }
   __syncthreads();
 }
