@@ -47,7 +47,8 @@ constexpr int kPtFirst = 1, kPtLast = 2, kPtEmpty = 4, kPtEnd = 8;
 struct PtSmem {
   uint64_t buf_full[kPtNBuf];       // rank 0: bytes of both CTAs' tokens
   uint64_t buf_empty[kPtNBuf];      // MMA commit to both CTAs after P V
-  uint64_t v_full[kPtNBuf];         // rank 0: bytes of both CTAs' peer values
+  uint64_t v_full[kPtNBuf];         // rank 0: both CTAs have the peer's values
+  uint64_t tail_full;               // the peer's values of a sequence's last page
   uint64_t q_full, q_empty;
   uint64_t s_full[kPtNBuf];
   uint64_t p_full[2], pv_done[2];   // by page parity
@@ -69,7 +70,6 @@ struct PtSmem {
 struct PtArgs {
   PagedView view;
   PagedOut o;
-  const __nv_bfloat16 *kv;
   int H;
   float scale_log2;
   int min_slots;
@@ -127,6 +127,10 @@ __device__ __forceinline__ uint64_t pt_desc_sw64(uint32_t saddr) {
   d |= (uint64_t)4u << 61;                              // layout: 64-byte swizzle
   return d;
 }
+// arrive on a barrier of this or the other CTA with bytes to come
+__device__ __forceinline__ void pt_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ bool pt_elect() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
@@ -141,42 +145,9 @@ __device__ __forceinline__ void pt_mma_pair(uint32_t d_tmem, uint64_t a, uint64_
       : "memory");
 }
 
-// 16 consecutive columns of this thread's TMEM lane
-__device__ __forceinline__ void pt_tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// 32 tokens of a page, from token t0 on: the map's 64-entry blocks from `src` on (`n` of them) to consecutive 4 KB at dst.
-// Whole warp.
-__device__ __forceinline__ void pt_copy(const CUtensorMap *blocks, const CUtensorMap *rows, int lane, int phys, int ntok, int t0,
-                                        int oob, int src, int n, uint32_t dst, uint32_t bar) {
-  if (ntok == kPage) {
-    if (lane == 0) pt_load_3d_pair(dst, blocks, 0, phys + t0, src, bar);
-  } else if (lane < kPtHalf / 4) {
-    int r4[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int t = t0 + 4 * lane + e;
-      r4[e] = t < ntok ? phys + t : oob;
-    }
-    for (int i = 0; i < n; ++i)
-      tc::tma_gather4_pair(dst + i * kPtBlk + 4 * lane * 128, rows, (src + i) * 64, r4[0], r4[1], r4[2], r4[3], bar);
-  }
-}
-
 struct PtMaps {
   CUtensorMap q;                    // [T][H][576] in boxes of 64 heads x 64 entries
   CUtensorMap keys, values;         // [9 blocks][tokens][64] in boxes of 32 tokens and 9 / 4 blocks
-  CUtensorMap row;                  // [tokens][576] in boxes of one token x 64 entries (gather4)
 };
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
@@ -195,7 +166,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     for (int i = 0; i < kPtNBuf; ++i) {
       tc::mbar_init(tc::smem_u32(&S->buf_full[i]), 1);
       tc::mbar_init(tc::smem_u32(&S->buf_empty[i]), 1);
-      tc::mbar_init(tc::smem_u32(&S->v_full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&S->v_full[i]), 2);
       tc::mbar_init(tc::smem_u32(&S->s_full[i]), 1);
     }
     tc::mbar_init(tc::smem_u32(&S->st_free), 4);
@@ -205,6 +176,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       tc::mbar_init(tc::smem_u32(&S->dec[i]), 4);
       tc::mbar_init(tc::smem_u32(&S->l_ready[i]), 4);
     }
+    tc::mbar_init(tc::smem_u32(&S->tail_full), 1);
     tc::mbar_init(tc::smem_u32(&S->q_full), 1);
     tc::mbar_init(tc::smem_u32(&S->q_empty), 1);
     tc::mbar_init(tc::smem_u32(&S->o_empty), 8);
@@ -218,7 +190,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     tc::prefetch_tmap(&tm.q);
     tc::prefetch_tmap(&tm.keys);
     tc::prefetch_tmap(&tm.values);
-    tc::prefetch_tmap(&tm.row);
   }
   if (warp == kPtWarpPV) {
     tc::tmem_alloc2(tc::smem_u32(&S->tmem_base), 512);
@@ -250,7 +221,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
 
   if (warp == kPtWarpKeys) {
     // ====================================================================== pages, keys and q
-    const int oob = a.view.num_blocks * kPage;             // a row outside the map: zero-filled
     const uint32_t buf_full_r0 = tc::map_to_rank(tc::smem_u32(&S->buf_full[0]), 0);
     const uint32_t q_full_r0 = tc::map_to_rank(tc::smem_u32(&S->q_full), 0);
     uint32_t ec = 0, c = 0, v = 0;
@@ -269,10 +239,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       if (!publish(phys, ntok, row, info)) return false;
       const uint32_t b = c % kPtNBuf;
       if (!pt_wait(tc::smem_u32(&S->buf_empty[b]), ((c / kPtNBuf) & 1u) ^ 1u, abort, status)) return false;
-      if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->buf_full[b]), 2u * kPtBuf);
+      if (lane == 0) {
+        if (rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->buf_full[b]), 2u * kPtBuf);
+        pt_load_3d_pair(tc::smem_u32(sBuf + b * kPtBuf), &tm.keys, 0, phys + kPtHalf * (int)rank, 0, buf_full_r0 + b * 8);
+      }
       __syncwarp();
-      pt_copy(&tm.keys, &tm.row, lane, phys, ntok, kPtHalf * (int)rank, oob, 0, 9, tc::smem_u32(sBuf + b * kPtBuf),
-              buf_full_r0 + b * 8);
       if (info & kPtFirst) {
         // q is overwritten once the previous segment's last QK^T has run
         if (v > 0 && !pt_wait(tc::smem_u32(&S->q_empty), (v - 1) & 1u, abort, status)) return false;
@@ -316,21 +287,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     if (lane == 0 && rank == 0) a.o.info[pair] = worker_info(a.view, S->plan);
   } else if (warp == kPtWarpValues) {
     // ====================================================================== the peer's values
-    const int oob = a.view.num_blocks * kPage;
+    // Token half t of a page lies in blocks 4t .. 4t + 3 of either CTA: its own tokens' values where the key copy put them,
+    // the peer's copied here.
     const uint32_t v_full_r0 = tc::map_to_rank(tc::smem_u32(&S->v_full[0]), 0);
-    const int dst = rank == 0 ? 4 : 0, src = rank == 0 ? 0 : 4;
-    uint32_t ec = 0, c = 0;
+    const uint32_t tail = tc::smem_u32(&S->tail_full);
+    const int other = (int)(rank ^ 1u);
+    uint32_t ec = 0, c = 0, tails = 0;
     int4 e;
     while (next_entry(ec, &e)) {
       if (e.w & kPtEnd) break;
       if (e.w & kPtEmpty) continue;
-      const uint32_t b = c % kPtNBuf;
+      const uint32_t b = c % kPtNBuf, full = v_full_r0 + b * 8;
+      uint8_t *buf = sBuf + b * kPtBuf;
+      const uint32_t dst = tc::smem_u32(buf + 4 * other * kPtBlk);
       // QK^T of this page has read the buffers
-      if (!pt_wait(tc::smem_u32(&S->s_full[c % kPtNBuf]), (c / kPtNBuf) & 1u, abort, status)) break;
-      if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->v_full[b]), 2u * 4u * kPtBlk);
+      if (!pt_wait(tc::smem_u32(&S->s_full[b]), (c / kPtNBuf) & 1u, abort, status)) break;
+      if (e.y == kPage) {
+        if (lane == 0) {
+          pt_expect_tx_cluster(full, 4u * kPtBlk);
+          pt_load_3d_pair(dst, &tm.values, 0, e.x + kPtHalf * other, 4 * (int)rank, full);
+        }
+      } else {
+        // A sequence's last page: P V takes its tokens in steps of 16 and leaves out the steps behind the last one; in that one
+        // the rows past the sequence become zeros here, so that 0 x (whatever the cache holds there) never enters a sum.
+        if (e.y > kPtHalf * other) {
+          if (lane == 0) {
+            tc::mbar_expect_tx(tail, 4u * kPtBlk);
+            pt_load_3d_pair(dst, &tm.values, 0, e.x + kPtHalf * other, 4 * (int)rank, tail);
+          }
+          __syncwarp();
+          if (!pt_wait(tail, tails++ & 1u, abort, status)) break;
+        }
+        const int last = (e.y - 1) / 16, t = last / 2;                       // the last step, and its token half
+        const int r0 = e.y - kPtHalf * t, rows = 16 * (last + 1) - e.y;      // rows r0 .. r0 + rows - 1 of that half
+        for (int i = lane; i < rows * 4 * 8; i += 32)
+          *reinterpret_cast<uint4 *>(buf + (4 * t + (i >> 3) % 4) * kPtBlk + (r0 + (i >> 5)) * 128 + (i & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) tc::mbar_arrive(full);
+          else tc::mbar_arrive_remote(full);
+        }
+      }
       __syncwarp();
-      pt_copy(&tm.values, &tm.row, lane, e.x, e.y, kPtHalf * (int)(rank ^ 1u), oob, src, 4,
-              tc::smem_u32(sBuf + b * kPtBuf + dst * kPtBlk), v_full_r0 + b * 8);
       ++c;
     }
   } else if (warp == kPtWarpQK || warp == kPtWarpPV) {
@@ -379,6 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
           if (info & kPtEmpty) continue;
           const uint32_t b = c % kPtNBuf;
           const bool first = info & kPtFirst;
+          const int steps = (__shfl_sync(0xffffffffu, e.y, 0) + 15) / 16;
           if (first) {
             if (segs > 0 && !pt_wait_cl(tc::smem_u32(&S->o_empty), (segs - 1) & 1u, abort, status)) break;
             ++segs;
@@ -391,11 +392,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
           if (pt_elect()) {
             // K steps of 16 tokens: token half (4 blocks apart) x two steps of 16 rows; both value halves share a step of P
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 4; ++k) {
+              if (k >= steps) break;
 #pragma unroll
               for (int p = 0; p < 2; ++p)
                 pt_mma_pair(tm + kPtTmemO + 128 * p, (k < 2 ? p0 : p1) + 2 * (k & 1),
                             vb + ((2 * p * kPtBlk + (k >> 1) * 4 * kPtBlk + (k & 1) * 16 * 128) >> 4), idesc, k > 0 || !first);
+            }
           }
           __syncwarp();
           tc::mma_commit_pair_w(tc::smem_u32(&S->buf_empty[b]), both);
@@ -646,13 +649,13 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
 EncodeTiledFn encode_tiled_fn();
 
 // bf16, [d2][d1][d0] with strides s1, s2 (entries), in boxes of b2 x b1 x 64 entries, 128-byte swizzle
-static bool pt_map(CUtensorMap *m, const void *base, uint32_t rank, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
+static bool pt_map(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
                    uint64_t s2, uint32_t b1, uint32_t b2) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1 * 2, s2 * 2};
   cuuint32_t box[3] = {64, b1, b2}, es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, es,
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -660,12 +663,11 @@ static bool pt_map(CUtensorMap *m, const void *base, uint32_t rank, uint64_t d0,
 // The main kernel of the latent cache; returns the workers (CTA pairs) through *workers for the join.
 dsa_status_t paged_mla_launch(const void *q, const void *kv, int H, float softmax_scale, const PagedView &view,
                               const PagedOut &o, int max_workers, cudaStream_t stream, int num_sms, int *workers) {
-  PtArgs a{view, o, (const __nv_bfloat16 *)kv, H, softmax_scale * 1.4426950408889634f, 2};
+  PtArgs a{view, o, H, softmax_scale * 1.4426950408889634f, 2};
   PtMaps tm;
   const uint64_t rows = (uint64_t)view.num_blocks * kPage, D = kPtD;
-  if (!pt_map(&tm.q, q, 3, D, (uint64_t)H, (uint64_t)view.T, D, D * H, 64, 1) ||
-      !pt_map(&tm.keys, kv, 3, 64, rows, 9, D, 64, kPtHalf, 9) || !pt_map(&tm.values, kv, 3, 64, rows, 9, D, 64, kPtHalf, 4) ||
-      !pt_map(&tm.row, kv, 2, D, rows, 1, D, 0, 1, 1)) {
+  if (!pt_map(&tm.q, q, D, (uint64_t)H, (uint64_t)view.T, D, D * H, 64, 1) ||
+      !pt_map(&tm.keys, kv, 64, rows, 9, D, 64, kPtHalf, 9) || !pt_map(&tm.values, kv, 64, rows, 9, D, 64, kPtHalf, 4)) {
     set_error("paged attention: cuTensorMapEncodeTiled failed");
     return DSA_ERR_CUDA;
   }
