@@ -268,11 +268,12 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a, 
 // Few rows have many parts each: kGroup = 8 up to 1,184 (row, head) pairs, one CTA of 8 warps per head (a 1M-token row, 74
 // parts of 128 heads: 8 us, 90 us with part after part); more rows have few parts: a warp per head (the 32-row decode batch,
 // 3.3 parts each, 28 us with 16 warps per head).
-constexpr int kPcThreads = 256, kPcWarps = kPcThreads / 32, kPcMaxParts = 160;
+constexpr int kPcThreads = 256, kPcWarps = kPcThreads / 32;
 
-template <typename T, int kGroup, int kN, bool kVec>
-__global__ void __launch_bounds__(kPcThreads) paged_combine_kernel(const PagedOut o, int workers, int H, int Dv) {
-  constexpr int kLane = kVec ? 4 : 1, kBlocks = kPcMaxParts / 32;
+// kBlocks: workers / 32, rounded up.  Four CTAs per SM, so that the decode batch's 4,096 warps run in one wave.
+template <typename T, int kGroup, int kN, bool kVec, int kBlocks>
+__global__ void __launch_bounds__(kPcThreads, 4) paged_combine_kernel(const PagedOut o, int workers, int H, int Dv) {
+  constexpr int kLane = kVec ? 4 : 1;
   __shared__ float s_acc[kGroup > 1 ? kPcWarps : 1][kN * kLane * 32];
   pdl_wait();
   pdl_trigger();
@@ -379,14 +380,14 @@ __global__ void __launch_bounds__(kPcThreads) paged_combine_kernel(const PagedOu
   if (o.lse && lane == 0) o.lse[(int64_t)row * H + h] = lse;
 }
 
-template <typename T, int kN, bool kVec>
+template <typename T, int kN, bool kVec, int kBlocks>
 static dsa_status_t combine_launch(const PagedOut &o, int workers, int T_rows, int H, int Dv, cudaStream_t stream) {
   const int rows = std::min(workers, T_rows);
   if ((int64_t)T_rows * H <= 8 * 148) {
-    DSA_LAUNCH_PDL("paged_combine_kernel", (paged_combine_kernel<T, 8, kN, kVec>), dim3(rows, H), dim3(kPcThreads), 0, stream, o,
+    DSA_LAUNCH_PDL("paged_combine_kernel", (paged_combine_kernel<T, 8, kN, kVec, kBlocks>), dim3(rows, H), dim3(kPcThreads), 0, stream, o,
                    workers, H, Dv);
   } else {
-    DSA_LAUNCH_PDL("paged_combine_kernel", (paged_combine_kernel<T, 1, kN, kVec>), dim3(rows, (H + kPcWarps - 1) / kPcWarps),
+    DSA_LAUNCH_PDL("paged_combine_kernel", (paged_combine_kernel<T, 1, kN, kVec, kBlocks>), dim3(rows, (H + kPcWarps - 1) / kPcWarps),
                    dim3(kPcThreads), 0, stream, o, workers, H, Dv);
   }
   return DSA_OK;
@@ -397,7 +398,8 @@ static size_t pg_al(size_t x) { return (x + 255) / 256 * 256; }
 
 // The most workers a launch uses; they size the workspace.  Value width tells the two paths apart: 512 is the latent
 // cache's (CTA pairs of a B200's 148 SMs), up to 128 the f32 path's.
-static int paged_max_workers(int Dv) { return Dv > 128 ? 74 : 148; }
+constexpr int kPagedPairs = 74, kPagedCtas = 148;
+static int paged_max_workers(int Dv) { return Dv > 128 ? kPagedPairs : kPagedCtas; }
 
 size_t paged_workspace_bytes(int H, int Dv) {
   const size_t w = (size_t)paged_max_workers(Dv);
@@ -455,7 +457,7 @@ dsa_status_t paged_attn_launch(const void *q, bool bf16, const void *kv, const v
     int workers = 0;
     const dsa_status_t st = paged_mla_launch(q, kv, H, scale, a.view, a.o, paged_max_workers(Dv), stream, num_sms, &workers);
     if (st != DSA_OK) return st;
-    return combine_launch<__nv_bfloat16, 4, true>(a.o, workers, b->total_q, H, Dv, stream);
+    return combine_launch<__nv_bfloat16, 4, true, (kPagedPairs + 31) / 32>(a.o, workers, b->total_q, H, Dv, stream);
   }
   const int workers = std::min(num_sms, paged_max_workers(Dv));
   // the fewest lanes that cover a row with four entries each, the fewest heads in steps of 4, 8, 16
@@ -465,8 +467,8 @@ dsa_status_t paged_attn_launch(const void *q, bool bf16, const void *kv, const v
   else if (D <= 64) st = simt_heads<16>(a, workers, stream);
   else st = simt_heads<32>(a, workers, stream);
   if (st != DSA_OK) return st;
-  if (Dv % 4 == 0) return combine_launch<float, 1, true>(a.o, workers, b->total_q, H, Dv, stream);
-  return combine_launch<float, 4, false>(a.o, workers, b->total_q, H, Dv, stream);
+  if (Dv % 4 == 0) return combine_launch<float, 1, true, (kPagedCtas + 31) / 32>(a.o, workers, b->total_q, H, Dv, stream);
+  return combine_launch<float, 4, false, (kPagedCtas + 31) / 32>(a.o, workers, b->total_q, H, Dv, stream);
 }
 
 }  // namespace dsa
