@@ -89,7 +89,17 @@ __device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int w
   const uint32_t before = block_exclusive_scan(mine, tmp, &total);
   // a worker for every min_slots page slots: fewer workers than that pay more for their partials than they save
   const uint32_t want = total / (uint32_t)min_slots;
-  const int np = want < 1u ? 1 : (want < (uint32_t)workers ? (int)want : workers);
+  int np = want < 1u ? 1 : (want < (uint32_t)workers ? (int)want : workers);
+  // Rows of one length (a batch of page lists): the same number of workers for each, so that none takes the end of one row and
+  // the beginning of the next.  A second segment costs what kSegment pages do (q, the epilogue, a pipeline that runs empty);
+  // 32 rows of 8 pages: 18 us over 64 workers, 22 us over 74.
+  constexpr uint32_t kSegment = 4;
+  const uint32_t n0 = total / (uint32_t)v.T;
+  const bool same = __syncthreads_and(mine == n0 * (uint32_t)(r1 - r0));
+  if (same && v.T <= np) {
+    const uint32_t each = (uint32_t)np / (uint32_t)v.T;
+    if (n0 / each <= total / (uint32_t)np + kSegment) np = (int)each * v.T;
+  }
   const bool any = worker < np;
   const uint32_t start = any ? (uint32_t)((uint64_t)worker * total / np) : total;
   const uint32_t end = any ? (uint32_t)((uint64_t)(worker + 1) * total / np) : total;
