@@ -323,9 +323,11 @@ __global__ void __launch_bounds__(kPcThreads, 4) paged_combine_kernel(const Page
       }
     };
     // the first parts' values are on their way while the weights are worked out
-    float v0[kN * kLane], v1[kN * kLane];
-    if (sub < n) load(sub, v0);
-    if (sub + kGroup < n) load(sub + kGroup, v1);
+    constexpr int kAhead = kN * kLane <= 4 ? 8 : 2;
+    float v[kAhead][kN * kLane];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (sub + j * kGroup < n) load(sub + j * kGroup, v[j]);
     float w[kBlocks], mx = -INFINITY, tot = 0.f;
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
@@ -343,19 +345,19 @@ __global__ void __launch_bounds__(kPcThreads, 4) paged_combine_kernel(const Page
     for (int off = 16; off; off >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, off);
     const float inv = tot != 0.f ? 1.f / tot : 0.f;
     lse = tot != 0.f ? mx + logf(tot) : -INFINITY;
+    for (int s0 = sub; s0 < n; s0 += kAhead * kGroup) {
 #pragma unroll
-    for (int i = 0; i < kBlocks; ++i) {
-      if (32 * i >= n) break;
-      const int top = min(32, n - 32 * i);
-      for (int l = sub; l < top; l += kGroup) {    // 32 is a multiple of kGroup
-        const int s = 32 * i + l;
-        const float ws = __shfl_sync(0xffffffffu, w[i], l) * inv;
+      for (int j = 0; j < kAhead; ++j) {
+        const int s = s0 + j * kGroup;             // the same for the whole warp
+        if (s >= n) break;
+        float ws = 0.f;
 #pragma unroll
-        for (int k = 0; k < kN * kLane; ++k) {
-          acc[k] = fmaf(ws, v0[k], acc[k]);
-          v0[k] = v1[k];
-        }
-        if (s + 2 * kGroup < n) load(s + 2 * kGroup, v1);
+        for (int i = 0; i < kBlocks; ++i)
+          if (s / 32 == i) ws = w[i];
+        ws = __shfl_sync(0xffffffffu, ws, s & 31) * inv;
+#pragma unroll
+        for (int k = 0; k < kN * kLane; ++k) acc[k] = fmaf(ws, v[j][k], acc[k]);
+        if (s + kAhead * kGroup < n) load(s + kAhead * kGroup, v[j]);
       }
     }
   }

@@ -176,112 +176,111 @@ __device__ __forceinline__ void rope_rows(const RopeArgs &a, const RopePartDev &
       piece[r] = ok ? (s < r0 ? s : s + 2 * np) : -1;
     }
   }
-  bool ready = false;
+  // a lane's heads are the same in every row (heads <= gh * NI)
+  int64_t x_off[NI], o_off[NI];
+  bool has[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int h = i * gh + h_first;
+    has[i] = h < heads;
+    x_off[i] = (int64_t)(head0 + h) * p.x_head;
+    o_off[i] = (int64_t)(head0 + h) * p.o_head;
+  }
   for (int rb = 0; rb < rows; rb += gr) {
     const int row = rb + r_first;
     const int64_t x_row = (int64_t)(row0 + row) * p.x_row;
-    const float2 *tr = tab.turn + row * half;
-    int64_t dst = -1;
-    for (int hb = 0; hb < heads; hb += gh * NI) {
-      float v[NI][NR][8];
+    float v[NI][NR][8];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int h = hb + i * gh + h_first;
-        const int64_t at = x_row + (int64_t)(head0 + h) * p.x_head;
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          if (row < rows && h < heads && piece[r] >= 0) {
-            rope_load8(p.x, at + 8 * piece[r], XT < 0 ? p.x_dt : XT, XT >= 0 || p.x_vec, v[i][r]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][r][e] = 0.f;
-          }
-        }
-      }
-      if (!ready) {
-        rope_tables(a, p, row0, rows, tab);
-        ready = true;
-      }
-      if (hb == 0 && row < rows) dst = tab.dst[row];
-      if (p.norm_len) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          float ss = 0.f;
-#pragma unroll
-          for (int r = 0; r < NR; ++r)
-            if (piece[r] >= n0 && piece[r] < n1)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) ss = fmaf(v[i][r][e], v[i][r][e], ss);
-#pragma unroll
-          for (int o = G / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float inv = 1.f / sqrtf(ss / (float)p.norm_len + p.eps);
-#pragma unroll
-          for (int r = 0; r < NR; ++r)
-            if (piece[r] >= n0 && piece[r] < n1) {
-              float w[8];
-              rope_load8(p.weight, 8 * (piece[r] - n0), p.w_dt, p.w_vec, w);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[i][r][e] *= inv * w[e];
-            }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < NR; r += 2) {
-        const int d = (r / 2) * G + lane;
-        if (d >= np || row >= rows) continue;
-        if (p.halves) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 c = tr[8 * d + e];
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-              const float x0 = v[i][r][e], x1 = v[i][r + 1][e];
-              v[i][r][e] = fmaf(x0, c.x, -x1 * c.y);
-              v[i][r + 1][e] = fmaf(x1, c.x, x0 * c.y);
-            }
-          }
+      for (int r = 0; r < NR; ++r) {
+        if (row < rows && has[i] && piece[r] >= 0) {
+          rope_load8(p.x, x_row + x_off[i] + 8 * piece[r], XT < 0 ? p.x_dt : XT, XT >= 0 || p.x_vec, v[i][r]);
         } else {
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 c = tr[4 * d + q * (half / 2) + e];
-#pragma unroll
-              for (int i = 0; i < NI; ++i) {
-                const float x0 = v[i][r + q][2 * e], x1 = v[i][r + q][2 * e + 1];
-                v[i][r + q][2 * e] = fmaf(x0, c.x, -x1 * c.y);
-                v[i][r + q][2 * e + 1] = fmaf(x1, c.x, x0 * c.y);
-              }
-            }
+          for (int e = 0; e < 8; ++e) v[i][r][e] = 0.f;
         }
       }
+    if (rb == 0) rope_tables(a, p, row0, rows, tab);
+    const int64_t dst = row < rows ? tab.dst[row] : -1;
+    const float2 *tr = tab.turn + row * half;
+    if (p.norm_len) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int h = hb + i * gh + h_first;
-        const bool live = dst >= 0 && h < heads;
-        if (p.scale) {
-          float am = 0.f;
-#pragma unroll
-          for (int r = 0; r < NR; ++r)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(v[i][r][e]));
-#pragma unroll
-          for (int o = G / 2; o; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-          float sc = am / 448.0f;
-          if (sc == 0.f) sc = 1.f;
-          if (live && lane == 0) p.scale[dst * p.H + head0 + h] = sc;
-#pragma unroll
-          for (int r = 0; r < NR; ++r)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][r][e] /= sc;
-        }
-        if (!live) continue;
-        const int64_t at = dst * p.o_row + (int64_t)(head0 + h) * p.o_head;
+        float ss = 0.f;
 #pragma unroll
         for (int r = 0; r < NR; ++r)
-          if (piece[r] >= 0)
-            rope_store8(p.out, at + 8 * piece[r], OT < 0 ? p.o_dt : OT, OT >= 0 || p.o_vec, v[i][r]);
+          if (piece[r] >= n0 && piece[r] < n1)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(v[i][r][e], v[i][r][e], ss);
+#pragma unroll
+        for (int o = G / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float inv = 1.f / sqrtf(ss / (float)p.norm_len + p.eps);
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+          if (piece[r] >= n0 && piece[r] < n1) {
+            float w[8];
+            rope_load8(p.weight, 8 * (piece[r] - n0), p.w_dt, p.w_vec, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i][r][e] *= inv * w[e];
+          }
       }
+    }
+#pragma unroll
+    for (int r = 0; r < NR; r += 2) {
+      const int d = (r / 2) * G + lane;
+      if (d >= np || row >= rows) continue;
+      if (p.halves) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 c = tr[8 * d + e];
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const float x0 = v[i][r][e], x1 = v[i][r + 1][e];
+            v[i][r][e] = fmaf(x0, c.x, -x1 * c.y);
+            v[i][r + 1][e] = fmaf(x1, c.x, x0 * c.y);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 c = tr[4 * d + q * (half / 2) + e];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+              const float x0 = v[i][r + q][2 * e], x1 = v[i][r + q][2 * e + 1];
+              v[i][r + q][2 * e] = fmaf(x0, c.x, -x1 * c.y);
+              v[i][r + q][2 * e + 1] = fmaf(x1, c.x, x0 * c.y);
+            }
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const bool live = dst >= 0 && has[i];
+      if (p.scale) {
+        float am = 0.f;
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(v[i][r][e]));
+#pragma unroll
+        for (int o = G / 2; o; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        float sc = am / 448.0f;
+        if (sc == 0.f) sc = 1.f;
+        if (live && lane == 0) p.scale[dst * p.H + head0 + i * gh + h_first] = sc;
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][r][e] /= sc;
+      }
+      if (!live) continue;
+      const int64_t at = dst * p.o_row + o_off[i];
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+        if (piece[r] >= 0)
+          rope_store8(p.out, at + 8 * piece[r], OT < 0 ? p.o_dt : OT, OT >= 0 || p.o_vec, v[i][r]);
     }
   }
 }
