@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a, 
   Smem &S = *reinterpret_cast<Smem *>(sm4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int worker = blockIdx.x, H = a.H, Dqk = a.Dqk, Dv = a.Dv;
-  const bool vk = (Dqk & 3) == 0, vv = (Dv & 3) == 0;
+  const bool vk = (Dqk & 3) == 0, vv = (Dv & 3) == 0, whole = Dqk == 4 * LT && Dv == 4 * LT;
   const int tg = lane / LT, d0 = 4 * (lane % LT);
   int first = 0;                                   // this lane's first head after ps_reduce
   {
@@ -133,13 +133,22 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a, 
       if (ntok <= 0) continue;                     // the same for the whole warp
       const float *kr = a.kv + ((int64_t)blk * kPage + t0) * Dqk, *vr = a.v + ((int64_t)blk * kPage + t0) * Dv;
       float4 k[kPsSteps], v[kPsSteps];
+      if (ntok >= kTok && whole) {                 // every lane has four entries of every token
+        const float *kp = kr + tg * Dqk + d0, *vp = vr + tg * Dv + d0;
 #pragma unroll
-      for (int s = 0; s < kPsSteps; ++s) {
-        const int t = s * TW + tg;
-        k[s] = v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t < ntok) {
-          k[s] = ps_load4(kr + (int64_t)t * Dqk, d0, Dqk, vk);
-          v[s] = ps_load4(vr + (int64_t)t * Dv, d0, Dv, vv);
+        for (int s = 0; s < kPsSteps; ++s) {
+          k[s] = __ldg(reinterpret_cast<const float4 *>(kp + s * TW * Dqk));
+          v[s] = __ldg(reinterpret_cast<const float4 *>(vp + s * TW * Dv));
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < kPsSteps; ++s) {
+          const int t = s * TW + tg;
+          k[s] = v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (t < ntok) {
+            k[s] = ps_load4(kr + t * Dqk, d0, Dqk, vk);
+            v[s] = ps_load4(vr + t * Dv, d0, Dv, vv);
+          }
         }
       }
       float z[kPsSteps][HV], mx[HV];
@@ -154,7 +163,8 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a, 
         ps_reduce<LT, HP>(d, lane);
 #pragma unroll
         for (int i = 0; i < HV; ++i) {
-          z[s][i] = s * TW + tg < ntok ? d[i] : -INFINITY;
+          z[s][i] = d[i];
+          if (s * TW + tg >= ntok) z[s][i] = -INFINITY;
           mx[i] = fmaxf(mx[i], z[s][i]);
         }
       }
