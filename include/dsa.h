@@ -351,7 +351,7 @@ DSA_API dsa_status_t dsa_cp_merge(const void *part_out, dsa_dtype_t dt, const fl
  *   count is out of range.
  * cached_lens, new_lens, done, seq_lens [num_seqs] int32; cu_q [num_seqs + 1] int32; block_table [num_seqs,
  * max_blocks_per_seq] int32; free_blocks [free_capacity] int32; free_count, free_left one int32; slots [total_q]
- * int64; positions [total_q] int32.  page_size 64.  Workspace: dsa_batch_workspace_size. */
+ * int64; positions [total_q] int32.  page_size 64, total_q <= 2^30.  Workspace: dsa_batch_workspace_size. */
 DSA_API dsa_status_t dsa_batch_workspace_size(dsa_op_t op, int32_t num_seqs, size_t *bytes);
 DSA_API dsa_status_t dsa_batch_extend(const int32_t *cached_lens, const int32_t *new_lens, int32_t num_seqs,
                                       int32_t page_size, int32_t max_blocks_per_seq, int32_t num_blocks, int32_t total_q,
@@ -383,7 +383,7 @@ DSA_API dsa_status_t dsa_batch_release(const int32_t *done, int32_t num_seqs, in
  *   x_dt f32 or bf16;  out_dt f32, bf16 or e4m3;  weight [norm_len] of w_dt f32 or bf16;  positions [T] int32
  *   (NULL only when no part rotates: every row is taken);  inv_freq [rope_len / 2] f64 radians per position, shared
  *   by the parts, whose non-zero rope_len must be equal;  slots [T] int64.
- * Supported: 1 to 4 parts; D a multiple of 8 in [8, 1024]; norm_off, norm_len and rope_off multiples of 8; rope_len a
+ * Supported: 1 to 4 parts; T <= 2^30; D a multiple of 8 in [8, 1024]; norm_off, norm_len and rope_off multiples of 8; rope_len a
  * multiple of 16 up to 256; out strides >= D.  The workspace only carries the status word (256 bytes). */
 typedef enum { DSA_ROPE_PAIRS = 0, DSA_ROPE_HALVES = 1 } dsa_rope_style_t;
 typedef struct {

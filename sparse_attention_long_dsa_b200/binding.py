@@ -387,6 +387,9 @@ def rope_part(x, out, *, weight=None, norm=(0, 0), eps: float = 1e-6, rope=(0, 0
         fail("slots must be [T] int64")
     if scale is not None and (str(scale.dtype) != "torch.float32" or scale.numel() != rows * H):
         fail("scale must be [rows, H] float32")
+    for name, t in (("weight", weight), ("slots", slots), ("scale", scale)):
+        if t is not None and t.device != x.device:
+            fail(f"{name} on {t.device}, x on {x.device}")
     if norm[1] and (weight is None or weight.numel() != norm[1] or str(weight.dtype)[6:] not in floats):
         fail("a norm needs a weight of its length, f32 or bf16")
     part = dsa_rope_part_t(x=x.data_ptr(), out=out.data_ptr(), weight=_ptr(weight), out_scale=_ptr(scale),

@@ -262,12 +262,7 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a, 
     }
     __syncthreads();
   }
-  // rows without a cached token: zeros, and -inf for the log-sum-exp
-  for (int r = worker; r < a.view.T; r += gridDim.x) {
-    if (row_slots(a.view, r) > 0) continue;
-    for (int i = tid; i < H * Dv; i += kPsThreads) ((float *)a.o.out)[(int64_t)r * H * Dv + i] = 0.f;
-    if (a.o.lse && tid < H) a.o.lse[(int64_t)r * H + tid] = -INFINITY;
-  }
+  zero_empty_rows<float>(a.view, a.o, H, Dv);
 }
 
 // ------------------------------------------------------------------------------------------------ join

@@ -632,14 +632,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     tc::fence_after_sync();
     tc::tmem_dealloc2(tmem, 512);
   }
-  // rows without a cached token: zeros, and -inf for the log-sum-exp
-  for (int r = blockIdx.x; r < a.view.T; r += gridDim.x) {
-    if (row_slots(a.view, r) > 0) continue;
-    uint4 *o = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o.out + (int64_t)r * a.H * kPtDv);
-    for (int i = threadIdx.x; i < a.H * kPtDv / 8; i += kPtThreads) o[i] = make_uint4(0, 0, 0, 0);
-    if (a.o.lse)
-      for (int i = threadIdx.x; i < a.H; i += kPtThreads) a.o.lse[(int64_t)r * a.H + i] = -INFINITY;
-  }
+  zero_empty_rows<__nv_bfloat16>(a.view, a.o, a.H, kPtDv);
 }
 
 // ------------------------------------------------------------------------------------------------ host
@@ -681,12 +674,12 @@ dsa_status_t paged_mla_launch(const void *q, const void *kv, int H, float softma
     set_error("no current CUDA device");
     return DSA_ERR_CUDA;
   }
+  if (cudaFuncSetAttribute(paged_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    set_error("paged attention: %s", cudaGetErrorString(cudaGetLastError()));
+    return DSA_ERR_CUDA;
+  }
   int pairs = resident[dev].load(std::memory_order_relaxed);
   if (pairs == 0) {
-    if (cudaFuncSetAttribute(paged_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-      set_error("paged attention: %s", cudaGetErrorString(cudaGetLastError()));
-      return DSA_ERR_CUDA;
-    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;

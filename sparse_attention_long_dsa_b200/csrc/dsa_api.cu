@@ -577,6 +577,7 @@ dsa_status_t dsa_batch_extend(const int32_t *cached_lens, const int32_t *new_len
   dsa_status_t st = check_tables(num_seqs, page_size, max_blocks_per_seq, num_blocks, free_capacity);
   if (st != DSA_OK) return st;
   CHECK_ARG(total_q >= 0, "total_q must be >= 0");
+  CHECK_SUP(total_q <= 1 << 30, "total_q must be at most 2^30 (got %d)", total_q);
   CHECK_ARG(cached_lens && new_lens && free_count && free_left && block_table && seq_lens && cu_q,
             "cached_lens, new_lens, free_count, free_left, block_table, seq_lens and cu_q are required");
   CHECK_ARG(free_capacity == 0 || free_blocks, "free_blocks is required");
@@ -651,6 +652,7 @@ static dsa_status_t check_rope_part(const dsa_rope_part_t *p, int i, int32_t T, 
 dsa_status_t dsa_qk_norm_rope(const dsa_rope_part_t *parts, int32_t num_parts, const int32_t *positions, int32_t T,
                               const double *inv_freq, void *ws, size_t ws_bytes, void *stream) {
   CHECK_ARG(T >= 0, "T must be >= 0");
+  CHECK_SUP(T <= 1 << 30, "T must be at most 2^30 (got %d)", T);
   CHECK_ARG(parts != nullptr, "parts is required");
   CHECK_SUP(num_parts >= 1 && num_parts <= 4, "num_parts must be in [1, 4] (got %d)", num_parts);
   if (T == 0) return DSA_OK;   // empty batch: nothing to enqueue, data pointers may be NULL

@@ -160,4 +160,28 @@ __device__ __forceinline__ int2 worker_info(const PagedView &v, const PagedPlan 
   return make_int2(p.row, worker_of_slot(p.start - (uint32_t)p.page, p));
 }
 
+// Rows without a cached token: zeros, and -inf for the log-sum-exp.  All warps of the grid call it (whole warps); row r belongs
+// to warp r % (their number), 32 rows looked at per load.
+template <typename T>
+__device__ __forceinline__ void zero_empty_rows(const PagedView &v, const PagedOut &o, int H, int Dv) {
+  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int64_t warps = (int64_t)gridDim.x * nw, mine = (int64_t)blockIdx.x * nw + (threadIdx.x >> 5);
+  for (int64_t r0 = mine; r0 < v.T; r0 += 32 * warps) {
+    const int64_t r = r0 + lane * warps;
+    uint32_t empty = __ballot_sync(0xffffffffu, r < v.T && row_slots(v, (int)r) == 0);
+    while (empty) {
+      const int64_t row = r0 + (__ffs(empty) - 1) * warps;
+      empty &= empty - 1;
+      T *out = (T *)o.out + row * H * Dv;
+      if (((int64_t)H * Dv * sizeof(T)) % 16 == 0) {
+        for (int i = lane; i < (int)(H * Dv * sizeof(T) / 16); i += 32) reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
+      } else {
+        for (int i = lane; i < H * Dv; i += 32) out[i] = T(0.f);
+      }
+      if (o.lse)
+        for (int i = lane; i < H; i += 32) o.lse[row * H + i] = -INFINITY;
+    }
+  }
+}
+
 }  // namespace dsa

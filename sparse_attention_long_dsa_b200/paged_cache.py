@@ -42,6 +42,7 @@ class PagedCache:
         self.cu_q = torch.zeros(num_seqs + 1, dtype=torch.int32, device=dv)
         self.free_blocks = torch.arange(num_blocks - 1, -1, -1, dtype=torch.int32, device=dv)   # block 0 on top
         self.free_count = torch.full((1,), num_blocks, dtype=torch.int32, device=dv)
+        self._rows = {}                              # total_q -> (slots, positions): a captured step keeps its own
         self.slots = self.positions = None
         self._one_each = torch.arange(num_seqs + 1, dtype=torch.int32, device=dv)
         size = max(B.dsa_batch_workspace_size(B.DSA_OP_BATCH_EXTEND, num_seqs),
@@ -51,9 +52,10 @@ class PagedCache:
     def extend(self, new_lens, total_q: int, stream=None):
         """A step of new_lens [num_seqs] tokens (device int32), total_q of them or fewer: grows the tables and lengths and
         fills cu_q, slots [total_q] and positions [total_q]."""
-        if self.slots is None or self.slots.numel() != total_q:
-            self.slots = torch.empty(total_q, dtype=torch.int64, device=self.device)
-            self.positions = torch.empty(total_q, dtype=torch.int32, device=self.device)
+        if total_q not in self._rows:
+            self._rows[total_q] = (torch.empty(total_q, dtype=torch.int64, device=self.device),
+                                   torch.empty(total_q, dtype=torch.int32, device=self.device))
+        self.slots, self.positions = self._rows[total_q]
         B.dsa_batch_extend(self.seq_lens, new_lens, PAGE, self.num_blocks, total_q, self.free_blocks, self.free_count,
                            self.block_table, self.seq_lens, self.cu_q, self.slots, self.positions, self.free_count, self.ws,
                            self.ws.numel(), stream)

@@ -181,6 +181,25 @@ def test_extend_refuses_a_step_that_does_not_fit(why):
     assert t.status() == B.DSA_OK                                       # read and cleared
 
 
+def test_extend_on_two_streams_at_once():
+    rng = np.random.default_rng(1)
+    add = [3000, 700, 1, 6000]
+    width, blocks, table, free = _random_tables(rng, [5, 0, 64, 63], add, spare=4)
+    a, b = (_Tables(4, width, blocks, free, table) for _ in range(2))
+    cached, new = _i32([5, 0, 64, 63]), _i32(add)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        for t, s in ((a, s1), (b, s2)):
+            with torch.cuda.stream(s):
+                t.extend(cached, new, sum(add), stream=s)
+    torch.cuda.synchronize()
+    ref_table, left, cu, slots, pos = _extend_ref([5, 0, 64, 63], add, table, free, sum(add))
+    for t in (a, b):
+        assert t.status() == B.DSA_OK and np.array_equal(t.table.cpu(), ref_table) and t.left.item() == left
+        assert np.array_equal(t.slots.cpu(), slots) and np.array_equal(t.pos.cpu(), pos)
+
+
 def test_extend_reports_bad_ids():
     """An id outside the pool on the stack, and one in an entry that a row needs: those pages' rows get no slot."""
     table = np.array([[5, -7, -7], [99, -7, -7], [1, -7, -7]])
@@ -259,6 +278,10 @@ def _positions(rng, t):
     (4, 2, 1024, (0, 1024), (768, 256), "f32", "f32"),
     (300, 1, 128, (0, 128), (0, 64), "bf16", "e4m3"),
     (2, 1, 72, (64, 8), (0, 48), "f32", "bf16"),
+    (3, 300, 64, (0, 64), (0, 32), "bf16", "bf16"),    # more heads than a CTA holds at a time
+    (2, 150, 256, (0, 0), (128, 128), "bf16", "e4m3"),
+    (2500, 128, 64, (0, 0), (0, 64), "bf16", "bf16"),  # several rows per CTA
+    (9001, 1, 576, (0, 512), (512, 64), "bf16", "f32"),
 ])
 def test_norm_and_rotation(style, t, h, d, norm, rope, xd, od):
     rng = np.random.default_rng(t * 1000 + d)
@@ -355,6 +378,31 @@ def test_rotation_in_place_matches_out_of_place():
     for src, dst in ((x, out), (y, y)):
         B.dsa_qk_norm_rope([B.rope_part(src, dst, weight=w, norm=(0, 128), rope=(64, 64), style="pairs")], pos, freq, ws, 256)
     assert torch.equal(out, y)
+
+
+def test_rotation_on_other_streams_and_in_a_graph():
+    x = torch.randn(40, 6, 64, device=DEV).bfloat16()
+    y = torch.randn(40, 6, 64, device=DEV).bfloat16()
+    pos, freq = torch.arange(40, dtype=torch.int32, device=DEV) * 31, torch.tensor(_freq(64), device=DEV)
+    outs = [torch.zeros_like(x) for _ in range(4)]
+    ws = [_zeros_ws(256) for _ in range(2)]
+    call = lambda i, o, w, s=None: B.dsa_qk_norm_rope([B.rope_part(i, o, rope=(0, 64))], pos, freq, w, 256, s)      # noqa: E731
+    call(x, outs[0], ws[0])
+    call(y, outs[1], ws[0])
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        call(x, outs[2], ws[0], s1)
+        call(y, outs[3], ws[1], s2)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(x, outs[2], ws[0])
+    pos.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[2], x)                                      # position 0 turns nothing
 
 
 def test_slots_past_the_output_are_reported():
@@ -530,7 +578,7 @@ def test_long_runs_of_rows_whose_lists_hold_nothing(heads, f32):
 
 @pytest.mark.parametrize("heads,f32", [(128, None), (32, None), (8, (64, 64))])
 def test_one_long_row_and_many_short_ones(heads, f32):
-    for lens in ([40001], [33] * 300, [1] * 200 + [30000] + [70] * 100, [0] * 7):
+    for lens in ([40001], [33] * 300, [1] * 200 + [30000] + [70] * 100, [0] * 7, ([0] * 50 + [65]) * 120, [0] * 40 + [500]):
         c = _Cache(lens, f32=f32, seed=len(lens))
         q = c.q(heads)
         out, lse = c.attend(q, 0.07)

@@ -48,6 +48,7 @@ def _extend(**kw):
     (dict(width=1 << 26), B.DSA_ERR_UNSUPPORTED),
     (dict(blocks=0), B.DSA_ERR_INVALID_ARG),
     (dict(rows=-1), B.DSA_ERR_INVALID_ARG),
+    (dict(rows=(1 << 30) + 1), B.DSA_ERR_UNSUPPORTED),
     (dict(cached=None), B.DSA_ERR_INVALID_ARG),
     (dict(free=None), B.DSA_ERR_INVALID_ARG),
     (dict(cap=-1), B.DSA_ERR_INVALID_ARG),
@@ -127,6 +128,7 @@ def test_rope_call_refusals():
     assert _rope([_part(), _part(rope_len=32)]) == B.DSA_ERR_INVALID_ARG and "differs" in _err()
     assert _rope([_part()] * 5) == B.DSA_ERR_UNSUPPORTED
     assert _rope([_part()], T=-1) == B.DSA_ERR_INVALID_ARG
+    assert _rope([_part(out_rows=1 << 31)], T=(1 << 30) + 1) == B.DSA_ERR_UNSUPPORTED
     assert _rope([_part()], ws_bytes=128) == B.DSA_ERR_WORKSPACE
     assert _rope([_part(x=None)], T=0) == B.DSA_OK                       # empty: checked only for its sizes
     assert _lib().dsa_qk_norm_rope(None, 1, P, 1, P, P, 256, None) == B.DSA_ERR_INVALID_ARG
