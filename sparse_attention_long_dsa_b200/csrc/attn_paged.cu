@@ -270,9 +270,8 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a, 
 // At most min(T, workers) rows are split, and CTA x finds the x-th of them in info; a warp takes a head (kGroup = 1) or every
 // kGroup-th part of one (the sums of the kGroup warps are added in a fixed order).  A lane holds kN pieces of the row (four
 // values each where Dv % 4 == 0, else single ones).  Bound by latency, so it is the number of warps in flight that counts.
-// Few rows have many parts each: kGroup = 8 up to 1,184 (row, head) pairs, one CTA of 8 warps per head (a 1M-token row, 74
-// parts of 128 heads: 8 us, 90 us with part after part); more rows have few parts: a warp per head (the 32-row decode batch,
-// 3.3 parts each, 28 us with 16 warps per head).
+// Few rows have many parts each: with eight warps per head a 1M-token row (74 parts of 128 heads) takes 8 us, part after part
+// 90 us.  Many rows have few: the 32-row decode batch (3.3 parts each) takes 5 us with a warp per head, 28 us with sixteen.
 constexpr int kPcThreads = 256, kPcWarps = kPcThreads / 32;
 
 // kBlocks: workers / 32, rounded up.  Four CTAs per SM, so that the decode batch's 4,096 warps run in one wave.
@@ -390,14 +389,19 @@ __global__ void __launch_bounds__(kPcThreads, 4) paged_combine_kernel(const Page
 template <typename T, int kN, bool kVec, int kBlocks>
 static dsa_status_t combine_launch(const PagedOut &o, int workers, int T_rows, int H, int Dv, cudaStream_t stream) {
   const int rows = std::min(workers, T_rows);
-  if ((int64_t)T_rows * H <= 8 * 148) {
-    DSA_LAUNCH_PDL("paged_combine_kernel", (paged_combine_kernel<T, 8, kN, kVec, kBlocks>), dim3(rows, H), dim3(kPcThreads), 0, stream, o,
-                   workers, H, Dv);
-  } else {
-    DSA_LAUNCH_PDL("paged_combine_kernel", (paged_combine_kernel<T, 1, kN, kVec, kBlocks>), dim3(rows, (H + kPcWarps - 1) / kPcWarps),
-                   dim3(kPcThreads), 0, stream, o, workers, H, Dv);
-  }
-  return DSA_OK;
+  auto go = [&](auto *kernel, int group) -> dsa_status_t {
+    const int heads = kPcWarps / group;
+    DSA_LAUNCH_PDL("paged_combine_kernel", kernel, dim3(rows, (H + heads - 1) / heads), dim3(kPcThreads), 0, stream, o, workers, H,
+                   Dv);
+    return DSA_OK;
+  };
+  // as many warps per (row, head) as run in one wave, 32 per SM (8 rows of 2,048 tokens, 128 heads: the whole call 18.9 us with
+  // four warps, 20.6 with one)
+  const int64_t pairs = (int64_t)rows * H, wave = 148 * 32;
+  if (8 * pairs <= wave) return go(paged_combine_kernel<T, 8, kN, kVec, kBlocks>, 8);
+  if (4 * pairs <= wave) return go(paged_combine_kernel<T, 4, kN, kVec, kBlocks>, 4);
+  if (2 * pairs <= wave) return go(paged_combine_kernel<T, 2, kN, kVec, kBlocks>, 2);
+  return go(paged_combine_kernel<T, 1, kN, kVec, kBlocks>, 1);
 }
 
 // ------------------------------------------------------------------------------------------------ host
