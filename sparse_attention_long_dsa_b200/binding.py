@@ -427,6 +427,19 @@ def dsa_qk_norm_rope(parts, positions, inv_freq, ws, ws_bytes: int, stream=None)
     _check((_lib or load()).dsa_qk_norm_rope(arr, len(parts), pos, T, freq, _ptr(ws), ws_bytes, _stream(stream)), w)
 
 
+def page_list_width(pages, rows: int) -> int:
+    """kb of a page list [rows, kb] int32 on the current device; 0 for None (every page)."""
+    import torch
+    if pages is None:
+        return 0
+    w = "dsa_paged_attn_decode"
+    if pages.dim() != 2:
+        raise DSAError(DSA_ERR_INVALID_ARG, w, f"pages of {pages.dim()} dimensions; expected [{rows}, kb]")
+    _shape(pages, (rows, pages.shape[1]), w)
+    _dense(w, torch.int32, pages)
+    return pages.shape[1]
+
+
 def dsa_paged_attn_decode(q, dt: int, kv_pool, v_pool, H: int, Dqk: int, Dv: int, softmax_scale: float, pages, kb: int,
                           batch: dsa_batch_t, out, lse, ws, ws_bytes: int, stream=None):
     """Attention of one new token per sequence over every cached page, or over its list of pages [B, kb]."""

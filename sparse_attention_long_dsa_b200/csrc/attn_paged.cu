@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kPcThreads, 4) paged_combine_kernel(const Page
     for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
-      w[i] = mx == -INFINITY ? 0.f : expf(w[i] - mx);
+      w[i] = w[i] == -INFINITY ? 0.f : expf(w[i] - mx);        // a part that is NaN makes its row NaN
       tot += w[i];
     }
 #pragma unroll

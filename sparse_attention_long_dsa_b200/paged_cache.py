@@ -42,7 +42,7 @@ class PagedCache:
         self.cu_q = torch.zeros(num_seqs + 1, dtype=torch.int32, device=dv)
         self.free_blocks = torch.arange(num_blocks - 1, -1, -1, dtype=torch.int32, device=dv)   # block 0 on top
         self.free_count = torch.full((1,), num_blocks, dtype=torch.int32, device=dv)
-        self._rows = {}                              # total_q -> (slots, positions): a captured step keeps its own
+        self._rows = {}                              # rows -> (slots, positions): kept, so that captured steps stay valid
         self.slots = self.positions = None
         self._one_each = torch.arange(num_seqs + 1, dtype=torch.int32, device=dv)
         size = max(B.dsa_batch_workspace_size(B.DSA_OP_BATCH_EXTEND, num_seqs),
@@ -51,11 +51,13 @@ class PagedCache:
 
     def extend(self, new_lens, total_q: int, stream=None):
         """A step of new_lens [num_seqs] tokens (device int32), total_q of them or fewer: grows the tables and lengths and
-        fills cu_q, slots [total_q] and positions [total_q]."""
-        if total_q not in self._rows:
-            self._rows[total_q] = (torch.empty(total_q, dtype=torch.int64, device=self.device),
-                                   torch.empty(total_q, dtype=torch.int32, device=self.device))
-        self.slots, self.positions = self._rows[total_q]
+        fills cu_q, slots [total_q] and positions [total_q].  Steps of similar sizes write the same buffers."""
+        cap = 1 << max(0, total_q - 1).bit_length()
+        if cap not in self._rows:
+            self._rows[cap] = (torch.empty(cap, dtype=torch.int64, device=self.device),
+                               torch.empty(cap, dtype=torch.int32, device=self.device))
+        slots, positions = self._rows[cap]
+        self.slots, self.positions = slots[:total_q], positions[:total_q]
         B.dsa_batch_extend(self.seq_lens, new_lens, PAGE, self.num_blocks, total_q, self.free_blocks, self.free_count,
                            self.block_table, self.seq_lens, self.cu_q, self.slots, self.positions, self.free_count, self.ws,
                            self.ws.numel(), stream)
@@ -95,7 +97,13 @@ class PagedCache:
     def attend(self, q, out, softmax_scale: float, pages=None, lse=None, stream=None):
         """q [num_seqs, heads, 576] over every cached token of its sequence, or over the tokens of the pages in pages
         [num_seqs, kb] (int32, -1: none); out [num_seqs, heads, 512].  Empty slots give zeros."""
-        kb = 0 if pages is None else pages.shape[1]
+        B._shape(q, (self.num_seqs, self.heads, LATENT), "attend")
+        B._shape(out, (self.num_seqs, self.heads, VALUE), "attend")
+        B._dense("attend", torch.bfloat16, q, out)
+        if lse is not None:
+            B._shape(lse, (self.num_seqs, self.heads), "attend")
+            B._dense("attend", torch.float32, lse)
+        kb = B.page_list_width(pages, self.num_seqs)
         B.dsa_paged_attn_decode(q, B.DSA_BF16, self.kv_pool, None, self.heads, LATENT, VALUE, softmax_scale, pages, kb,
                                 self.decode_batch(), out, lse, self.ws, self.ws.numel(), stream)
 

@@ -191,7 +191,7 @@ class DeviceBatch:
         """Attention of a decode batch over every cached page, or over the pages in pages [total_q, kb] (such as
         block_pages gives), without expanding them to token positions."""
         wl = self.wl
-        kb = 0 if pages is None else pages.shape[1]
+        kb = B.page_list_width(pages, wl.total_q)
         need = B.dsa_workspace_size(B.DSA_OP_PAGED_DECODE, self.batch, kb, wl.H, wl.Dv)
         if getattr(self, "_paged_ws", None) is None:
             self._paged_ws = torch.zeros(need, dtype=torch.uint8, device=self.device)

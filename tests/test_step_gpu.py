@@ -621,6 +621,21 @@ def test_same_bits_again_without_lse_on_other_streams_and_with_two_calls_at_once
     assert torch.equal(o1, ref1) and torch.equal(o2, ref2)
 
 
+@pytest.mark.parametrize("heads,f32", [(128, None), (4, (64, 64))])
+def test_a_head_that_is_nan_stays_nan_and_alone(heads, f32):
+    """A NaN in one head's query: NaN in its result and its log-sum-exp, whether the row is split or not; the other heads keep
+    their bits."""
+    c = _Cache([5, 9000], f32=f32, seed=91)
+    q = c.q(heads)
+    out, lse = c.attend(q, 0.1)
+    bad = q.clone()
+    bad[:, 2, 3] = float("nan")
+    o2, l2 = c.attend(bad, 0.1)
+    assert o2[:, 2].isnan().all() and l2[:, 2].isnan().all()
+    keep = [h for h in range(heads) if h != 2]
+    assert torch.equal(o2[:, keep], out[:, keep]) and torch.equal(l2[:, keep], lse[:, keep])
+
+
 def test_lengths_and_tables_may_change_under_a_captured_graph():
     c = _Cache([700, 64, 1], seed=12)
     q = c.q(128)
@@ -832,6 +847,40 @@ def test_a_captured_step_replays_as_the_cache_grows():
             cache.check_status()
             assert cache.seq_lens.tolist() == want.tolist()
             _view(cache, heads).check(q, 0.07, out, lse)
+
+
+def test_steps_of_many_sizes_share_buffers_and_keep_their_addresses():
+    cache = PagedCache(2, 40, 30, 4)
+    seen, total = {}, 0
+    for t in (1, 2, 3, 5, 8, 7, 9, 100, 65, 128, 3, 1, 0):
+        cache.extend(_i32([t // 2, t - t // 2]), t)
+        cache.check_status()
+        assert cache.slots.shape == cache.positions.shape == (t,)
+        at = (cache.slots.data_ptr(), cache.positions.data_ptr())
+        assert seen.setdefault(t, at) == at
+        total += t
+        assert cache.positions.tolist() == [cache.seq_lens[0].item() - t // 2 + i for i in range(t // 2)] + \
+            [cache.seq_lens[1].item() - (t - t // 2) + i for i in range(t - t // 2)]
+    assert cache.seq_lens.sum().item() == total and len(cache._rows) <= 8
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=lambda q: q[:1]), dict(q=lambda q: q[:, :2]), dict(q=lambda q: q.float()), dict(out=lambda o: o[:1]),
+    dict(out=lambda o: o.float()), dict(lse=lambda x: x[:1]), dict(lse=lambda x: x.bfloat16()),
+    dict(pages=lambda p: p[:1]), dict(pages=lambda p: p.long()), dict(pages=lambda p: p[0]), dict(pages=lambda p: p.cpu()),
+])
+def test_attend_refuses_tensors_of_other_shapes_and_types(change):
+    cache = PagedCache(2, 4, 2, 4)
+    a = dict(q=torch.zeros((2, 4, 576), dtype=torch.bfloat16, device=DEV),
+             out=torch.zeros((2, 4, 512), dtype=torch.bfloat16, device=DEV), lse=torch.zeros((2, 4), device=DEV),
+             pages=_i32([[0, 1], [1, -1]]))
+    cache.attend(a["q"], a["out"], 0.1, pages=a["pages"], lse=a["lse"])
+    cache.check_status()
+    for k, f in change.items():
+        a[k] = f(a[k])
+    with pytest.raises(B.DSAError) as e:
+        cache.attend(a["q"], a["out"], 0.1, pages=a["pages"], lse=a["lse"])
+    assert e.value.status == B.DSA_ERR_INVALID_ARG
 
 
 @pytest.mark.parametrize("kind", ["mla", "f32"])
