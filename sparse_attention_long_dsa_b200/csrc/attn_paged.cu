@@ -11,8 +11,11 @@
 // HP heads are summed over the LT lanes by halving exchanges (each step halves the values a lane carries: HP - 1 shuffles
 // instead of HP log2(LT)), which leaves each (token, head) in one lane for the softmax; the weights come back through a
 // warp's own shared memory.  Warps are joined at the end of a segment, in their order.  Tokens past the sequence are not
-// loaded: what the cache holds there may be anything.  Bound by HBM up to about 8 heads (8 flop per byte and head), then by
-// the FMA and shuffle issue.
+// loaded: what the cache holds there may be anything.
+// Bound by the issue of loads, FMAs and shuffles from two warps per scheduler (q, output, keys and values of a batch take most
+// of the registers).  16 rows of 256 - 8,192 tokens (61,000 in all, 31 MB at 4 heads of 64): 14 us, the bytes alone 4.8 us;
+// 16 heads of 64: 26 us, 16 heads of 128 (62 MB): 38 us; one row of 131,072 tokens, 4 heads of 64: 20 us (67 MB, 3.3 TB/s).
+// Two CTAs per SM with half the registers, and the next batch's keys loaded a batch ahead, were both slower.
 #include <algorithm>
 
 #include "paged.cuh"

@@ -6,21 +6,32 @@
 // prefetches the next KV block while the current one is computed, partial results are merged by a cross-block reduction).
 //
 // A token costs 1152 bytes of HBM and 2 x 128 x 1088 products whatever the number of heads (missing heads are zero rows of
-// q): 0.176 ns of copy bandwidth against 0.085 ns of a pair's tensor time over 74 pairs, so the kernel is built to keep the
-// copies running.  Work split of a pair (rank r = 0, 1), one page of 64 tokens at a time, over the flat range of page slots
-// that paged.cuh gives it:
-//   * resolve: one warp per CTA walks the slots (32 table entries per load) and publishes the pages that hold tokens to the
-//              other roles through a ring: physical row, tokens, row, first / last of its segment;
-//   * keys   : each CTA copies ITS 32 tokens of the page, all 576 entries, into one of three buffers [9 blocks][32 tokens]
-//              [128 B] by nine tiled TMA copies (a page is contiguous).  The last page of a sequence comes by gather4
-//              instead, whose rows past the sequence are zero-filled: nothing stale reaches the tensor cores;
-//   * QK^T   : M = 128 heads (64 per CTA), N = 64 tokens (32 from each CTA), K = 576;
+// q): 0.176 ns of copy bandwidth against 0.169 ns of tensor peak.  So copies and matrix instructions both have to run without
+// a pause.  Split of a pair's work (rank r = 0, 1), one page of 64 tokens at a time, over the flat range of page slots that
+// paged.cuh gives it; 384 threads per CTA:
+//   * keys   : one warp walks the slots (32 table entries per load, the next 32 ahead), publishes the pages that hold tokens
+//              to the other roles through a ring (physical row, tokens, row, first / last of its segment) and copies this
+//              CTA's 32 tokens of the page, all 576 entries, by one tiled TMA copy into one of four buffers [9 blocks]
+//              [32 tokens][128 B] (a page is contiguous; pieces of a page gathered row by row cost 2 us on a last page);
+//   * QK^T   : M = 128 heads (64 per CTA), N = 64 tokens (32 from each CTA), K = 576, up to four pages ahead of P V;
 //   * values : each CTA needs 256 of the 512 value entries of all 64 tokens: the peer's 32 tokens' half (16 KB, an L2 hit)
-//              is copied over the blocks that QK^T no longer needs, as soon as it has run;
-//   * softmax: 4 warps per CTA, one (head, 32-token half) per thread; O is rescaled in TMEM only when the running maximum
-//              grows by more than 2^8 (exact: the final division uses the same reference);
-//   * P V    : two N = 256 MMAs over K = 64 tokens; O (64 heads x 512 fp32 per CTA) stays in TMEM.
-// P is rounded to bf16 for P V, as the tensor cores take it; the sum l keeps the unrounded weights in fp32.
+//              is copied over the blocks that QK^T no longer needs, as soon as it has run.  In a sequence's last page the
+//              rows past its end become zeros before P V reads them, and whole steps of 16 tokens past it are left out;
+//   * softmax: two groups of four warps take alternate pages, one (head, 32-token half) per thread.  Both use one reference
+//              per head, and O is rescaled in TMEM only when a score outgrows it by 2^8 (exact: the final division uses the
+//              same reference);
+//   * P V    : two N = 256 MMAs for each 16 tokens; O (64 heads x 512 fp32 per CTA) stays in TMEM.  P lies half in the
+//              page's ninth block, half in one of two 4 KB buffers, so that two pages of it are in flight.
+// P is rounded to bf16 for P V, as the tensor cores take it (2^-8 of a weight); the sum l keeps the unrounded weights in fp32.
+//
+// Measured on one B200, the join included: 1 row of 1,048,576 tokens 280 us (4.3 TB/s of keys, 1.04 PFLOP/s) in short bursts,
+// 334 us in a loop of seconds, where the 1000 W cap holds the SM clock at 1.3 - 1.6 GHz; 32 rows of 4K - 32K tokens 137 us,
+// 165 us in a loop (the kernel alone 126 us: DRAM 56 %, tensor pipe 54 % busy); 61 rows up to 8K, 16 heads, 69 us.  A page
+// takes 1.2 us of a pair: 0.83 us is what DRAM gives, 1,425 cycles the matrix instructions (QK^T 36 steps of 25.3 cycles, held
+// by the operand reads at N = 64; P V 8 of 64.3), and what is left is the way of a buffer through copy, QK^T, softmax, P V.
+// What lost: QK^T of two pages as one N = 128 instruction (32.3 cycles a step, but a page then waits for the next one: 299 us,
+// 343 in a loop), the latent entries split over the pair with partial scores exchanged (831 us: 32 KB through distributed
+// shared memory take 1,950 cycles), pages brought into L2 ahead of their copies (no gain with four buffers).
 #include <algorithm>
 #include <atomic>
 
@@ -75,8 +86,8 @@ struct PtArgs {
   int min_slots;
 };
 
-// Waits of whole warps.  A phase that is already complete costs one test and a branch (about 40 cycles; the general form with
-// its loop and warp vote inline took 200, and there are ten of them on the way of a page).  false: the wait ran out.
+// Waits of whole warps.  A phase that is already complete costs one test and a branch: with what stands between two waits 100 to
+// 160 cycles, where the general form (its loop and a warp vote inline) took 150 to 250; ten of them lie on the way of a page.
 __device__ __noinline__ bool pt_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *status) {
   return tc::mbar_wait(bar, parity, abort, status);
 }

@@ -13,6 +13,11 @@
 //
 // Angles: theta in turns, reduced to [-1/2, 1/2] in 64 bits, because at position 10^6 a 32-bit product is off by 0.06
 // radians; the sine and cosine of the reduced angle are 32-bit and computed once per (row, i) for all heads of a CTA.
+//
+// One read and one write of every row: bound by HBM, and for few rows by latency.  A 16,384-row prompt (128 query heads' 64
+// rotated entries, latent rows, 64 indexer heads, indexer key; 984 MB) takes 195 us, 5.0 TB/s: the query part moves pieces of
+// 128 bytes at strides of 384 and 1,152 (torch's strided copy of them reaches 1.8 TB/s); dense rows of 128 take 6.1 TB/s.  The
+// 32 rows of a decode step take 8.1 us.  Four CTAs of 256 threads per SM: 217 us with three.
 #include <algorithm>
 
 #include "common.cuh"
