@@ -1,14 +1,17 @@
 // One-token attention over the paged cache: how its kernels walk the pages of a batch.
 //
 // Every row of a decode batch has a number of page slots (all pages of its sequence, or the kb entries of its page
-// list).  The slots of all rows, one row after another, form one flat range of P slots, and worker w of np takes
-// the slots [floor(w P / np), floor((w + 1) P / np)): contiguous, equal to within one page whatever the lengths
-// are, and known to every worker from the lengths alone (they stay on the device).  The piece of a row inside a
-// worker's range is a segment.  A segment that holds its whole row writes the row's result; the others write a
-// partial result, normalised with its log-sum-exp, to a slot of the workspace: slot 2w + 1 when the row starts in
-// worker w (and goes on), 2w when it started before.  Worker w notes in info[w] the row that ends in it after
-// starting elsewhere, and the combine kernel joins that row's partials in the workers' order, so results do not
-// depend on timing.
+// list).  The slots of all rows, one row after another, form one flat range of P slots, and every worker takes a
+// contiguous piece of it that it finds from the lengths alone (they stay on the device), in one of two ways:
+//   * the flat split: worker w of np takes [floor(w P / np), floor((w + 1) P / np)), equal to within one page whatever
+//     the lengths are;
+//   * the split by rows: every row is cut into pieces of its own, so that no worker takes the end of one row and the
+//     beginning of the next.
+// The piece of a row inside a worker's range is a segment.  A segment that holds its whole row writes the row's
+// result; the others write a partial result, normalised with its log-sum-exp, to a slot of the workspace: slot
+// 2w + 1 when the row starts in worker w (and goes on), 2w when it started before.  Worker w notes in info[w] the
+// row that ends in it after starting elsewhere, and the combine kernel joins that row's partials in the workers'
+// order, so results do not depend on timing.
 #pragma once
 
 #include "common.cuh"
@@ -36,8 +39,9 @@ struct PagedOut {
 struct PagedPlan {
   uint32_t total;               // P
   uint32_t start, end;          // this worker's slots
-  int np;                       // workers that have any
+  int np;                       // the flat split: workers that have any
   int row, page;                // where `start` lies
+  int first;                    // split by rows: the worker that `row` starts in; -1: the flat split
 };
 
 __device__ __forceinline__ int row_slots(const PagedView &v, int row) {
@@ -78,6 +82,34 @@ __device__ __forceinline__ int worker_of_slot(uint32_t f, const PagedPlan &p) {
   return (int)((((uint64_t)f + 1) * (uint64_t)p.np - 1) / p.total);
 }
 
+// The split by rows; thread r has row r, of `mine` slots behind `before` others.  c0, c1, c2: the longest pieces to try; c2 needs
+// at most W workers, the others at most 2 W.  false: a piece would be longer than `limit`.
+__device__ __forceinline__ bool split_rows(int worker, uint32_t mine, uint32_t before, uint32_t total, uint32_t limit, uint32_t W,
+                                           uint32_t c0, uint32_t c1, uint32_t c2, uint32_t *tmp, PagedPlan *p) {
+  // 10 bits for each count of workers: W <= 148
+  const uint32_t n0 = (mine + c0 - 1) / c0, n1 = (mine + c1 - 1) / c1, n2 = (mine + c2 - 1) / c2;
+  uint32_t sums;
+  uint32_t at = block_exclusive_scan(n0 | n1 << 10 | n2 << 20, tmp, &sums);
+  uint32_t n = n2, c = c2, shift = 20;
+  if (((sums >> 10) & 1023u) <= W && c1 <= c) n = n1, c = c1, shift = 10;
+  if ((sums & 1023u) <= W && c0 <= c) n = n0, shift = 0;
+  at = (at >> shift) & 1023u;
+  const uint32_t size = mine / max(n, 1u), longer = mine - size * n;       // the first `longer` pieces have size + 1 slots
+  if (__syncthreads_or(size + (longer > 0) > limit)) return false;
+  const uint32_t w = (uint32_t)worker, piece = w - at;
+  if (w >= at && piece < n) {                          // one thread: the worker's piece is of its row
+    const uint32_t from = piece * size + min(piece, longer);
+    p->start = before + from;
+    p->end = before + from + size + (piece < longer);
+    p->row = (int)threadIdx.x;
+    p->page = (int)from;
+    p->first = (int)at;
+  }
+  if (threadIdx.x == 0 && w >= ((sums >> shift) & 1023u)) p->start = p->end = total;
+  __syncthreads();
+  return true;
+}
+
 // Every thread of the block calls this (blockDim.x a multiple of 32, at most 1024); `tmp` holds 33 words.
 __device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int workers, int min_slots, uint32_t *tmp,
                                            PagedPlan *p) {
@@ -90,15 +122,31 @@ __device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int w
   // a worker for every min_slots page slots: fewer workers than that pay more for their partials than they save
   const uint32_t want = total / (uint32_t)min_slots;
   int np = want < 1u ? 1 : (want < (uint32_t)workers ? (int)want : workers);
-  // Rows of one length (a batch of page lists): the same number of workers for each, so that none takes the end of one row and
-  // the beginning of the next.  A second segment costs what kSegment pages do (q, the epilogue, a pipeline that runs empty);
-  // 32 rows of 8 pages: 18 us over 64 workers, 22 us over 74.
+  // A second segment costs a worker what kSegment pages do (q, the epilogue, a pipeline that runs empty).  So no worker takes
+  // the end of one row and the beginning of the next where the longest piece is not longer than the flat split's by more than
+  // that.  Rows of one length (a batch of page lists) only need a number of workers that is the same for each: 32 rows of 8
+  // pages 18 us, 22 us with the flat split.  Others, of n slots each, are cut into ceil(n / c) pieces, c the smallest of three
+  // lengths that needs no more workers than there are.  Latent cache: 8 rows of 2 - 3 pages 13.7 us, 18.2 with the flat split; 26
+  // rows of one page or none 11.9, 15.3; 16 rows of 1 - 13 pages 18.0, 20.7.  f32: 16 rows of 4 - 128 pages, 4 heads of 64 13.2,
+  // 13.9; 16 heads of 128 33.6, 38.4.  Where it turns out not to pay, looking for it costs 0.3 us.
   constexpr uint32_t kSegment = 4;
-  const uint32_t n0 = total / (uint32_t)v.T;
-  const bool same = __syncthreads_and(mine == n0 * (uint32_t)(r1 - r0));
-  if (same && v.T <= np) {
-    const uint32_t each = (uint32_t)np / (uint32_t)v.T;
-    if (n0 / each <= total / (uint32_t)np + kSegment) np = (int)each * v.T;
+  if (v.T > 1) {
+    const uint32_t n0 = total / (uint32_t)v.T;
+    const bool same = __syncthreads_and(mine == n0 * (uint32_t)(r1 - r0));
+    const int rows = same ? v.T : __syncthreads_count(mine > 0);
+    const uint32_t limit = total / (uint32_t)np + kSegment;
+    if (same && rows <= workers) {
+      const uint32_t each = rows < np ? (uint32_t)np / (uint32_t)rows : 1u;
+      if (n0 / each <= limit) np = (int)each * rows;
+    }
+    if (!same && per == 1 && rows > 1 && rows <= workers && total > (uint32_t)np) {
+      const uint32_t R = (uint32_t)rows, W = max((uint32_t)np, R), avg = (total + R - 1) / R;
+      const uint32_t c0 = (avg + W / R - 1) / (W / R), c1 = (total + W - R / 2 - 1) / (W - R / 2);
+      const uint32_t c2 = W > R ? (total + W - R - 1) / (W - R) : total;
+      if (min(min(c0, c1), c2) <= limit && split_rows(worker, mine, before, total, limit, W, max(c0, (uint32_t)min_slots),
+                                                      max(c1, (uint32_t)min_slots), max(c2, (uint32_t)min_slots), tmp, p))
+        return;
+    }
   }
   const bool any = worker < np;
   const uint32_t start = any ? (uint32_t)((uint64_t)worker * total / np) : total;
@@ -108,6 +156,7 @@ __device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int w
     p->np = np;
     p->start = start;
     p->end = end;
+    p->first = -1;
   }
   if (start < end && start >= before && start < before + mine) {     // one thread; no worker without slots reads row and page
     uint32_t at = before;
@@ -157,7 +206,7 @@ __device__ __forceinline__ int2 worker_info(const PagedView &v, const PagedPlan 
   if (p.start >= p.end || p.page == 0) return make_int2(-1, 0);
   const int n = row_slots(v, p.row);
   if ((uint32_t)(n - p.page) > p.end - p.start) return make_int2(-1, 0);      // the row goes on in the next worker
-  return make_int2(p.row, worker_of_slot(p.start - (uint32_t)p.page, p));
+  return make_int2(p.row, p.first >= 0 ? p.first : worker_of_slot(p.start - (uint32_t)p.page, p));
 }
 
 // Rows without a cached token: zeros, and -inf for the log-sum-exp.  All warps of the grid call it (whole warps); row r belongs

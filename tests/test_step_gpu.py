@@ -621,6 +621,24 @@ def test_same_bits_again_without_lse_on_other_streams_and_with_two_calls_at_once
     assert torch.equal(o1, ref1) and torch.equal(o2, ref2)
 
 
+@pytest.mark.parametrize("heads,f32", [(128, None), (20, None), (4, (64, 64))])
+@pytest.mark.parametrize("rows,lo,hi,empty", [
+    (2, 16, 33, 0), (3, 100, 400, 0), (8, 87, 175, 0), (16, 0, 794, 0), (26, 1, 54, 9), (74, 1, 60, 0), (75, 1, 60, 1),
+    (75, 1, 60, 0), (148, 64, 130, 0), (200, 1, 400, 150), (300, 1, 3000, 270), (390, 1, 90, 350), (6, 1035, 2070, 1),
+    (40, 1, 900, 0), (30, 60, 70, 0),
+])
+def test_batches_of_rows_of_different_lengths(heads, f32, rows, lo, hi, empty):
+    """Small batches are cut into pieces of rows, others into equal ranges of pages: both sides, and where they meet."""
+    rng = np.random.default_rng(rows * 7 + hi)
+    lens = rng.integers(lo, hi + 1, rows)
+    lens[rng.permutation(rows)[:empty]] = 0
+    c = _Cache(lens.tolist(), f32=f32, seed=rows)
+    q = c.q(heads)
+    out, lse = c.attend(q, 0.07)
+    B.dsa_read_device_status(c.ws)
+    c.check(q, 0.07, out, lse)
+
+
 @pytest.mark.parametrize("heads,f32", [(128, None), (4, (64, 64))])
 def test_a_head_that_is_nan_stays_nan_and_alone(heads, f32):
     """A NaN in one head's query: NaN in its result and its log-sum-exp, whether the row is split or not; the other heads keep
