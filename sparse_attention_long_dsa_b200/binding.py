@@ -293,7 +293,7 @@ def dsa_cp_merge(part_out, dt: int, part_lse, G: int, T: int, H: int, Dv: int, o
 def _dense(what: str, dtype, *tensors):
     """Addresses of dense tensors of one dtype on the current device."""
     import torch
-    cur = torch.cuda.current_device() if tensors[0].is_cuda else -1
+    cur = torch._C._cuda_getDevice() if tensors[0].is_cuda else -1
     for t in tensors:
         if t.dtype is not dtype:
             raise DSAError(DSA_ERR_INVALID_ARG, what, f"a {t.dtype} tensor; expected {dtype}")
@@ -411,7 +411,7 @@ def dsa_qk_norm_rope(parts, positions, inv_freq, ws, ws_bytes: int, stream=None)
     w = "dsa_qk_norm_rope"
     if not 1 <= len(parts) <= 4:
         raise DSAError(DSA_ERR_UNSUPPORTED, w, f"{len(parts)} parts; 1 to 4 are taken")
-    T, cur = parts[0].rows, torch.cuda.current_device()
+    T, cur = parts[0].rows, torch._C._cuda_getDevice()       # the parts hold CUDA tensors: CUDA is up
     for p in parts:
         if p.rows != T:
             raise DSAError(DSA_ERR_INVALID_ARG, w, f"parts of {T} and {p.rows} rows")

@@ -13,8 +13,8 @@
 // warp's own shared memory.  Warps are joined at the end of a segment, in their order.  Tokens past the sequence are not
 // loaded: what the cache holds there may be anything.
 // Bound by the issue of loads, FMAs and shuffles from two warps per scheduler (q, output, keys and values of a batch take most
-// of the registers).  16 rows of 256 - 8,192 tokens (61,000 in all, 31 MB at 4 heads of 64): 14 us, the bytes alone 4.8 us;
-// 16 heads of 64: 26 us, 16 heads of 128 (62 MB): 38 us; one row of 131,072 tokens, 4 heads of 64: 20 us (67 MB, 3.3 TB/s).
+// of the registers).  16 rows of 256 - 8,192 tokens (61,000 in all, 31 MB at 4 heads of 64): 13 us, the bytes alone 4.8 us;
+// 16 heads of 64: 23 us, 16 heads of 128 (64 MB): 34 us; one row of 131,072 tokens, 4 heads of 64: 20 us (67 MB, 3.3 TB/s).
 // Two CTAs per SM with half the registers, and the next batch's keys loaded a batch ahead, were both slower.
 #include <algorithm>
 

@@ -13,7 +13,7 @@
 // not fit changes neither the tables nor the stack; the expansion is one thread per four query rows.  The first row of
 // a page (pos % 64 == 0, always one of the step's rows when the page is new) also writes the table entry, so pages
 // need no pass of their own.  Bound by latency (a few bytes per sequence and 12 per row): 4.4 us for a decode step of 32
-// sequences, 6.3 us for two 8,192-row chunks beside 14 of them, 8.6 us for 64 prompts of 1 to 16,384 rows (6.7 MB).
+// sequences, 6.3 us for two 8,192-row chunks beside 16 decodes, 8.6 us for 64 prompts of 1 to 16,384 rows (6.7 MB).
 #include <algorithm>
 
 #include "common.cuh"
