@@ -572,30 +572,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       const float l_tot = S->x[g][h] + S->x[g][h + 64];
       const float inv = l_tot != 0.f ? 1.f / l_tot : 0.f;
       if (ok) {
-        // bf16 results go out as they are (64 bytes per lane and step); partial ones through a per-warp tile of 32 rows x 16
-        // entries in the P buffer (16-byte group j of a row at j ^ (row / 2 & 3)), in 64-byte pieces of rows
+        // Through a per-warp tile of 32 rows x 64 bytes in the P buffer (16-byte group j of a row at j ^ (row / 2 & 3)), in
+        // 64-byte pieces of rows: 32 entries of a result, 16 of a partial one
         float *stg = reinterpret_cast<float *>(sP) + (warp & 3) * 512;
         const int head0 = 64 * (int)rank + 32 * (warp & 1), col0 = 256 * half;
         if (head0 < a.H) {
-          for (int cc = 0; cc < 8; ++cc) {
-            float ov[32];
-            tc::tmem_ld32(tmem + lane_base + kPtTmemO + 32 * cc, ov);
-            tc::tmem_wait_ld();
-            const int col = col0 + 32 * cc;
+          auto store = [&](const float (&ov)[32], int col) {
             if (part < 0) {
-              __nv_bfloat16 *o = out + ((int64_t)row * a.H + head) * kPtDv + col;
-              if (head < a.H) {
+              uint8_t *tile = reinterpret_cast<uint8_t *>(stg);
 #pragma unroll
-                for (int q8 = 0; q8 < 4; ++q8) {
-                  uint32_t w[4];
+              for (int q8 = 0; q8 < 4; ++q8) {
+                uint32_t w[4];
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(ov[8 * q8 + 2 * i] * inv, ov[8 * q8 + 2 * i + 1] * inv);
-                    w[i] = *reinterpret_cast<const uint32_t *>(&b);
-                  }
-                  *reinterpret_cast<uint4 *>(o + 8 * q8) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int i = 0; i < 4; ++i) {
+                  const __nv_bfloat162 b = __floats2bfloat162_rn(ov[8 * q8 + 2 * i] * inv, ov[8 * q8 + 2 * i + 1] * inv);
+                  w[i] = *reinterpret_cast<const uint32_t *>(&b);
                 }
+                *reinterpret_cast<uint4 *>(tile + lane * 64 + ((q8 ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
               }
+              __syncwarp();
+#pragma unroll
+              for (int it = 0; it < 4; ++it) {
+                const int r = 8 * it + (lane >> 2), j = lane & 3;
+                if (head0 + r < a.H)
+                  *reinterpret_cast<uint4 *>(out + ((int64_t)row * a.H + head0 + r) * kPtDv + col + 8 * j) =
+                      *reinterpret_cast<const uint4 *>(tile + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+              }
+              __syncwarp();
             } else {
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh) {
@@ -616,6 +619,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
                 __syncwarp();
               }
             }
+          };
+          for (int cc = 0; cc < 8; cc += 2) {
+            float o0[32], o1[32];
+            tc::tmem_ld32(tmem + lane_base + kPtTmemO + 32 * cc, o0);
+            tc::tmem_ld32(tmem + lane_base + kPtTmemO + 32 * cc + 32, o1);
+            tc::tmem_wait_ld();
+            store(o0, col0 + 32 * cc);
+            store(o1, col0 + 32 * cc + 32);
           }
         }
         if (half == 0 && head < a.H) {
