@@ -49,11 +49,11 @@ constexpr int kPtGroup = 128;                      // threads of a softmax group
 constexpr int kPtWarpKeys = 8, kPtWarpQK = 9, kPtWarpPV = 10, kPtWarpValues = 11;
 constexpr uint32_t kPtBlk = kPtHalf * 128;         // one 64-entry block of a CTA's 32 tokens: 4 KB
 constexpr uint32_t kPtBuf = 9 * kPtBlk;
-constexpr uint32_t kPtQ = 9 * 8192;
+constexpr uint32_t kPtQSize = 9 * 8192;
 constexpr uint32_t kPtP = 4096;                    // half of P: [64 heads][32 tokens] bf16, 64-byte swizzle
 constexpr uint32_t kPtTmemO = 0, kPtTmemS = 256;
 constexpr float kPtRescale = 8.0f;
-constexpr int kPtFirst = 1, kPtLast = 2, kPtEmpty = 4, kPtEnd = 8;
+constexpr int kPtFirst = 1, kPtLast = 2, kPtEmpty = 4, kPtEnd = 8, kPtQ = 16;     // kPtQ: q of an empty segment was loaded
 
 struct PtSmem {
   uint64_t buf_full[kPtNBuf];       // rank 0: bytes of both CTAs' tokens
@@ -165,7 +165,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     paged_mla_kernel(const __grid_constant__ PtMaps tm, const PtArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sQ = smem;                              // [9 blocks][64 heads][128 B]
-  uint8_t *sBuf = sQ + kPtQ;                       // 4 x [9 blocks][32 tokens][128 B]
+  uint8_t *sBuf = sQ + kPtQSize;                       // 4 x [9 blocks][32 tokens][128 B]
   uint8_t *sP = sBuf + kPtNBuf * kPtBuf;           // second halves of two pages' P; epilogue staging
   PtSmem *S = (PtSmem *)(sP + 2 * kPtP);
 
@@ -246,6 +246,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       ++ec;
       return true;
     };
+    auto load_q = [&](int row) {
+      if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->q_full), 2u * kPtQSize);
+      __syncwarp();
+      if (lane < 9) pt_load_3d_pair(tc::smem_u32(sQ + lane * 8192), &tm.q, lane * 64, 64 * (int)rank, row, q_full_r0);
+      ++v;
+    };
+    bool q_loaded = false;
     auto page = [&](int phys, int ntok, int row, int info) -> bool {
       if (!publish(phys, ntok, row, info)) return false;
       const uint32_t b = c % kPtNBuf;
@@ -255,14 +262,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         pt_load_3d_pair(tc::smem_u32(sBuf + b * kPtBuf), &tm.keys, 0, phys + kPtHalf * (int)rank, 0, buf_full_r0 + b * 8);
       }
       __syncwarp();
-      if (info & kPtFirst) {
+      if ((info & kPtFirst) && !q_loaded) {
         // q is overwritten once the previous segment's last QK^T has run
-        if (v > 0 && !pt_wait(tc::smem_u32(&S->q_empty), (v - 1) & 1u, abort, status)) return false;
-        if (lane == 0 && rank == 0) tc::mbar_expect_tx(tc::smem_u32(&S->q_full), 2u * kPtQ);
-        __syncwarp();
-        if (lane < 9) pt_load_3d_pair(tc::smem_u32(sQ + lane * 8192), &tm.q, lane * 64, 64 * (int)rank, row, q_full_r0);
-        ++v;
+        if (!pt_wait(tc::smem_u32(&S->q_empty), (v - 1) & 1u, abort, status)) return false;
+        load_q(row);
       }
+      if (info & kPtFirst) q_loaded = false;
       ++c;
       return true;
     };
@@ -270,6 +275,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     int row, sa, sb, part;
     bool ok = true;
     while (ok && walk.next(a.view, S->plan, pair, &row, &sa, &sb, &part)) {
+      // the first segment's q is on its way while its pages are looked up (later ones' pages come first)
+      if (v == 0) {
+        load_q(row);
+        q_loaded = true;
+      }
       const int n = row_tokens(a.view, row, status);
       const int tag = (part + 1) << 8;
       // 32 slots per load, the next 32 loaded ahead; one page is held back until it is known whether another follows
@@ -292,7 +302,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         blk = blk_n;
         nt = nt_n;
       }
-      if (ok) ok = h_ntok ? page(h_phys, h_ntok, row, flags | kPtLast | tag) : publish(0, 0, row, kPtEmpty | tag);
+      if (ok) ok = h_ntok ? page(h_phys, h_ntok, row, flags | kPtLast | tag) : publish(0, 0, row, kPtEmpty | tag | (q_loaded ? kPtQ : 0));
+      q_loaded = false;
     }
     if (ok) publish(0, 0, 0, kPtEnd);
     if (lane == 0 && rank == 0) a.o.info[pair] = worker_info(a.view, S->plan);
@@ -361,6 +372,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
         while (next_entry(ec, &e)) {
           const int info = __shfl_sync(0xffffffffu, e.w, 0);
           if (info & kPtEnd) break;
+          if (info & kPtQ) {
+            if (!pt_wait(tc::smem_u32(&S->q_full), segs++ & 1u, abort, status)) break;
+            tc::mma_commit_pair_w(tc::smem_u32(&S->q_empty), both);
+          }
           if (info & kPtEmpty) continue;
           const uint32_t b = c % kPtNBuf;
           if ((info & kPtFirst) && !pt_wait(tc::smem_u32(&S->q_full), segs++ & 1u, abort, status)) break;
@@ -686,7 +701,7 @@ dsa_status_t paged_mla_launch(const void *q, const void *kv, int H, float softma
     set_error("paged attention: cuTensorMapEncodeTiled failed");
     return DSA_ERR_CUDA;
   }
-  constexpr size_t smem = kPtQ + kPtNBuf * kPtBuf + 2 * kPtP + sizeof(PtSmem);
+  constexpr size_t smem = kPtQSize + kPtNBuf * kPtBuf + 2 * kPtP + sizeof(PtSmem);
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   // as many CTA pairs as can be resident at once, found once per device (threads that race on the first call
   // compute the same number)
