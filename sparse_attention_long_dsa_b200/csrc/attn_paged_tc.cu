@@ -44,6 +44,10 @@ constexpr int kPtD = 576, kPtDv = 512;
 constexpr int kPtHalf = kPage / 2;
 constexpr int kPtNBuf = 4;                         // page buffers, and score tiles
 constexpr int kPtRing = 8;                         // published pages in flight
+// Fewest pages of a worker, and the longest row that stays whole: a page takes 0.9 us of a pair, cutting a row 3 us.  One row of 4
+// pages 13.0 us whole, 14.3 in two pieces; 16 rows of 5 pages 14.6, 16.7; one row of 8 pages 14.5 us in pieces of two, 16.0 of
+// four; of 128 pages 20.4 in pieces of two, 19.2 of four (one row of 64 times min_slots takes twice as many).
+constexpr uint32_t kPtMinSlots = 2, kPtWhole = 5;
 constexpr int kPtThreads = 384;                    // softmax x 8, keys, QK^T, P V, values
 constexpr int kPtGroup = 128;                      // threads of a softmax group (4 warps)
 constexpr int kPtWarpKeys = 8, kPtWarpQK = 9, kPtWarpPV = 10, kPtWarpValues = 11;
@@ -83,7 +87,6 @@ struct PtArgs {
   PagedOut o;
   int H;
   float scale_log2;
-  int min_slots;
 };
 
 // Waits of whole warps.  A phase that is already complete costs one test and a branch: with what stands between two waits 100 to
@@ -216,7 +219,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
   // inputs come from earlier work on the stream
   pdl_wait();
   pdl_trigger();
-  plan_pages(a.view, pair, npairs, a.min_slots, S->tmp, &S->plan);
+  plan_pages(a.view, pair, npairs, kPtMinSlots, kPtWhole, S->tmp, &S->plan);
 
   // next entry of the ring, for a whole warp: false ends the role (the end of the work, or a wait that ran out)
   auto next_entry = [&](uint32_t &ec, int4 *e) -> bool {
@@ -693,7 +696,7 @@ static bool pt_map(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, u
 // The main kernel of the latent cache; returns the workers (CTA pairs) through *workers for the join.
 dsa_status_t paged_mla_launch(const void *q, const void *kv, int H, float softmax_scale, const PagedView &view,
                               const PagedOut &o, int max_workers, cudaStream_t stream, int num_sms, int *workers) {
-  PtArgs a{view, o, H, softmax_scale * 1.4426950408889634f, 2};
+  PtArgs a{view, o, H, softmax_scale * 1.4426950408889634f};
   PtMaps tm;
   const uint64_t rows = (uint64_t)view.num_blocks * kPage, D = kPtD;
   if (!pt_map(&tm.q, q, D, (uint64_t)H, (uint64_t)view.T, D, D * H, 64, 1) ||

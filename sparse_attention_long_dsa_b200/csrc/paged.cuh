@@ -83,11 +83,12 @@ __device__ __forceinline__ int worker_of_slot(uint32_t f, const PagedPlan &p) {
 }
 
 // The split by rows; thread r has row r, of `mine` slots behind `before` others.  c0, c1, c2: the longest pieces to try; c2 needs
-// at most W workers, the others at most 2 W.  false: a piece would be longer than `limit`.
+// at most W workers, the others at most 2 W; rows of at most `whole` slots stay whole.  false: a piece would be longer than `limit`.
 __device__ __forceinline__ bool split_rows(int worker, uint32_t mine, uint32_t before, uint32_t total, uint32_t limit, uint32_t W,
-                                           uint32_t c0, uint32_t c1, uint32_t c2, uint32_t *tmp, PagedPlan *p) {
+                                           uint32_t whole, uint32_t c0, uint32_t c1, uint32_t c2, uint32_t *tmp, PagedPlan *p) {
   // 10 bits for each count of workers: W <= 148
-  const uint32_t n0 = (mine + c0 - 1) / c0, n1 = (mine + c1 - 1) / c1, n2 = (mine + c2 - 1) / c2;
+  uint32_t n0 = (mine + c0 - 1) / c0, n1 = (mine + c1 - 1) / c1, n2 = (mine + c2 - 1) / c2;
+  if (mine <= whole) n0 = n1 = n2 = min(mine, 1u);
   uint32_t sums;
   uint32_t at = block_exclusive_scan(n0 | n1 << 10 | n2 << 20, tmp, &sums);
   uint32_t n = n2, c = c2, shift = 20;
@@ -111,17 +112,19 @@ __device__ __forceinline__ bool split_rows(int worker, uint32_t mine, uint32_t b
 }
 
 // Every thread of the block calls this (blockDim.x a multiple of 32, at most 1024); `tmp` holds 33 words.
-__device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int workers, int min_slots, uint32_t *tmp,
-                                           PagedPlan *p) {
+__device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int workers, uint32_t min_slots, uint32_t whole,
+                                           uint32_t *tmp, PagedPlan *p) {
   const int nt = blockDim.x, per = (v.T + nt - 1) / nt;
   const int r0 = min(v.T, (int)threadIdx.x * per), r1 = min(v.T, r0 + per);
   uint32_t mine = 0;
   for (int r = r0; r < r1; ++r) mine += (uint32_t)row_slots(v, r);
   uint32_t total;
   const uint32_t before = block_exclusive_scan(mine, tmp, &total);
-  // a worker for every min_slots page slots: fewer workers than that pay more for their partials than they save
-  const uint32_t want = total / (uint32_t)min_slots;
-  int np = want < 1u ? 1 : (want < (uint32_t)workers ? (int)want : workers);
+  // A worker for every min_slots page slots, and rows of at most `whole` slots in one piece: cutting a row costs partial results
+  // and their join.  One row of 64 min_slots and more: twice the slots, because its join grows with its pieces (latent
+  // cache, 8,192 tokens: 20.9 -> 19.4 us; f32: 10.5 -> 9.0 us).
+  const uint32_t want = total / (v.T == 1 && total >= 64 * min_slots ? 2 * min_slots : min_slots);
+  int np = want < 1u || (v.T == 1 && total <= whole) ? 1 : (want < (uint32_t)workers ? (int)want : workers);
   // A second segment costs a worker what kSegment pages do (q, the epilogue, a pipeline that runs empty).  So no worker takes
   // the end of one row and the beginning of the next where the longest piece is not longer than the flat split's by more than
   // that.  Rows of one length (a batch of page lists) only need a number of workers that is the same for each: 32 rows of 8
@@ -136,15 +139,15 @@ __device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int w
     const int rows = same ? v.T : __syncthreads_count(mine > 0);
     const uint32_t limit = total / (uint32_t)np + kSegment;
     if (same && rows <= workers) {
-      const uint32_t each = rows < np ? (uint32_t)np / (uint32_t)rows : 1u;
+      const uint32_t each = rows < np && n0 > whole ? (uint32_t)np / (uint32_t)rows : 1u;
       if (n0 / each <= limit) np = (int)each * rows;
     }
     if (!same && per == 1 && rows > 1 && rows <= workers && total > (uint32_t)np) {
       const uint32_t R = (uint32_t)rows, W = max((uint32_t)np, R), avg = (total + R - 1) / R;
       const uint32_t c0 = (avg + W / R - 1) / (W / R), c1 = (total + W - R / 2 - 1) / (W - R / 2);
       const uint32_t c2 = W > R ? (total + W - R - 1) / (W - R) : total;
-      if (min(min(c0, c1), c2) <= limit && split_rows(worker, mine, before, total, limit, W, max(c0, (uint32_t)min_slots),
-                                                      max(c1, (uint32_t)min_slots), max(c2, (uint32_t)min_slots), tmp, p))
+      if (min(min(c0, c1), c2) <= limit &&
+          split_rows(worker, mine, before, total, limit, W, whole, max(c0, min_slots), max(c1, min_slots), max(c2, min_slots), tmp, p))
         return;
     }
   }
