@@ -82,21 +82,43 @@ __device__ __forceinline__ int worker_of_slot(uint32_t f, const PagedPlan &p) {
   return (int)((((uint64_t)f + 1) * (uint64_t)p.np - 1) / p.total);
 }
 
+// The threads that make a plan: one warp (up to 32 rows: no barriers, 0.5 us less), or the block.
+template <bool kWarp>
+struct PlanThreads {
+  uint32_t *tmp;                // 33 words, for the block
+  __device__ __forceinline__ int count() const { return kWarp ? 32 : (int)blockDim.x; }
+  __device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t *total) const {
+    if (!kWarp) return block_exclusive_scan(v, tmp, total);
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if ((int)threadIdx.x >= o) x += y;
+    }
+    *total = __shfl_sync(0xffffffffu, x, 31);
+    return x - v;
+  }
+  __device__ __forceinline__ bool all(bool x) const { return kWarp ? __all_sync(0xffffffffu, x) : __syncthreads_and(x); }
+  __device__ __forceinline__ bool any(bool x) const { return kWarp ? __any_sync(0xffffffffu, x) : __syncthreads_or(x); }
+  __device__ __forceinline__ int that(bool x) const { return kWarp ? __popc(__ballot_sync(0xffffffffu, x)) : __syncthreads_count(x); }
+};
+
 // The split by rows; thread r has row r, of `mine` slots behind `before` others.  c0, c1, c2: the longest pieces to try; c2 needs
 // at most W workers, the others at most 2 W; rows of at most `whole` slots stay whole.  false: a piece would be longer than `limit`.
-__device__ __forceinline__ bool split_rows(int worker, uint32_t mine, uint32_t before, uint32_t total, uint32_t limit, uint32_t W,
-                                           uint32_t whole, uint32_t c0, uint32_t c1, uint32_t c2, uint32_t *tmp, PagedPlan *p) {
+template <bool kWarp>
+__device__ __forceinline__ bool split_rows(const PlanThreads<kWarp> &th, int worker, uint32_t mine, uint32_t before, uint32_t total, uint32_t limit, uint32_t W,
+                                           uint32_t whole, uint32_t c0, uint32_t c1, uint32_t c2, PagedPlan *p) {
   // 10 bits for each count of workers: W <= 148
   uint32_t n0 = (mine + c0 - 1) / c0, n1 = (mine + c1 - 1) / c1, n2 = (mine + c2 - 1) / c2;
   if (mine <= whole) n0 = n1 = n2 = min(mine, 1u);
   uint32_t sums;
-  uint32_t at = block_exclusive_scan(n0 | n1 << 10 | n2 << 20, tmp, &sums);
+  uint32_t at = th.scan(n0 | n1 << 10 | n2 << 20, &sums);
   uint32_t n = n2, c = c2, shift = 20;
   if (((sums >> 10) & 1023u) <= W && c1 <= c) n = n1, c = c1, shift = 10;
   if ((sums & 1023u) <= W && c0 <= c) n = n0, shift = 0;
   at = (at >> shift) & 1023u;
   const uint32_t size = mine / max(n, 1u), longer = mine - size * n;       // the first `longer` pieces have size + 1 slots
-  if (__syncthreads_or(size + (longer > 0) > limit)) return false;
+  if (th.any(size + (longer > 0) > limit)) return false;
   const uint32_t w = (uint32_t)worker, piece = w - at;
   if (w >= at && piece < n) {                          // one thread: the worker's piece is of its row
     const uint32_t from = piece * size + min(piece, longer);
@@ -107,19 +129,18 @@ __device__ __forceinline__ bool split_rows(int worker, uint32_t mine, uint32_t b
     p->first = (int)at;
   }
   if (threadIdx.x == 0 && w >= ((sums >> shift) & 1023u)) p->start = p->end = total;
-  __syncthreads();
   return true;
 }
 
-// Every thread of the block calls this (blockDim.x a multiple of 32, at most 1024); `tmp` holds 33 words.
-__device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int workers, uint32_t min_slots, uint32_t whole,
-                                           uint32_t *tmp, PagedPlan *p) {
-  const int nt = blockDim.x, per = (v.T + nt - 1) / nt;
+template <bool kWarp>
+__device__ __forceinline__ void make_plan(const PlanThreads<kWarp> &th, const PagedView &v, int worker, int workers,
+                                          uint32_t min_slots, uint32_t whole, PagedPlan *p) {
+  const int nt = th.count(), per = kWarp ? 1 : (v.T + nt - 1) / nt;
   const int r0 = min(v.T, (int)threadIdx.x * per), r1 = min(v.T, r0 + per);
   uint32_t mine = 0;
   for (int r = r0; r < r1; ++r) mine += (uint32_t)row_slots(v, r);
   uint32_t total;
-  const uint32_t before = block_exclusive_scan(mine, tmp, &total);
+  const uint32_t before = th.scan(mine, &total);
   // A worker for every min_slots page slots, and rows of at most `whole` slots in one piece: cutting a row costs partial results
   // and their join.  One row of 64 min_slots and more: twice the slots, because its join grows with its pieces (latent
   // cache, 8,192 tokens: 20.9 -> 19.4 us; f32: 10.5 -> 9.0 us).
@@ -135,8 +156,8 @@ __device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int w
   constexpr uint32_t kSegment = 4;
   if (v.T > 1) {
     const uint32_t n0 = total / (uint32_t)v.T;
-    const bool same = __syncthreads_and(mine == n0 * (uint32_t)(r1 - r0));
-    const int rows = same ? v.T : __syncthreads_count(mine > 0);
+    const bool same = th.all(mine == n0 * (uint32_t)(r1 - r0));
+    const int rows = same ? v.T : th.that(mine > 0);
     const uint32_t limit = total / (uint32_t)np + kSegment;
     if (same && rows <= workers) {
       const uint32_t each = rows < np && n0 > whole ? (uint32_t)np / (uint32_t)rows : 1u;
@@ -147,7 +168,7 @@ __device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int w
       const uint32_t c0 = (avg + W / R - 1) / (W / R), c1 = (total + W - R / 2 - 1) / (W - R / 2);
       const uint32_t c2 = W > R ? (total + W - R - 1) / (W - R) : total;
       if (min(min(c0, c1), c2) <= limit &&
-          split_rows(worker, mine, before, total, limit, W, whole, max(c0, min_slots), max(c1, min_slots), max(c2, min_slots), tmp, p))
+          split_rows(th, worker, mine, before, total, limit, W, whole, max(c0, min_slots), max(c1, min_slots), max(c2, min_slots), p))
         return;
     }
   }
@@ -173,6 +194,13 @@ __device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int w
     p->row = r;
     p->page = (int)(start - at);
   }
+}
+
+// Every thread of the block calls this (blockDim.x a multiple of 32, at most 1024); `tmp` holds 33 words.
+__device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int workers, uint32_t min_slots, uint32_t whole,
+                                           uint32_t *tmp, PagedPlan *p) {
+  if (v.T > 32) make_plan(PlanThreads<false>{tmp}, v, worker, workers, min_slots, whole, p);
+  else if (threadIdx.x < 32) make_plan(PlanThreads<true>{tmp}, v, worker, workers, min_slots, whole, p);
   __syncthreads();
 }
 
