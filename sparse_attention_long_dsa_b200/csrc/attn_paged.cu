@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a) 
     }
     __syncthreads();
   }
-  zero_empty_rows<float>(a.view, a.o, H, Dv);
+  zero_empty_rows<float>(a.view, a.o, H, Dv, (int64_t)blockIdx.x * kPsWarps + warp, (int64_t)gridDim.x * kPsWarps);
 }
 
 // ------------------------------------------------------------------------------------------------ join

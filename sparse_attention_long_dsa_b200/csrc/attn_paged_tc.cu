@@ -359,7 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       ++c;
     }
   } else if (warp == kPtWarpQK || warp == kPtWarpPV) {
-    // ====================================================================== MMA issuers (rank 0, whole warps)
+    // ====================================================================== MMA issuers (rank 0, whole warps); empty rows (rank 1)
     // Two warps, because issuing a page's MMAs and waiting for its operands takes one warp longer (about 1,900 cycles) than
     // the tensor core needs to run them (1,425).  A page's score tile is free when its buffer is.
     if (rank == 0) {
@@ -438,6 +438,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
       tc::mma_commit_pair_local_w(tc::smem_u32(&S->drain[which]));
       volatile int no_abort = 0;
       __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&S->drain[which]), 0, &no_abort, status));
+    } else {
+      zero_empty_rows<__nv_bfloat16>(a.view, a.o, a.H, kPtDv, 2 * pair + (warp == kPtWarpPV), 2 * npairs);
     }
   } else {
     // ====================================================================== softmax + epilogue (two groups of 4 warps)
@@ -672,7 +674,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
     tc::fence_after_sync();
     tc::tmem_dealloc2(tmem, 512);
   }
-  zero_empty_rows<__nv_bfloat16>(a.view, a.o, a.H, kPtDv);
 }
 
 // ------------------------------------------------------------------------------------------------ host

@@ -240,12 +240,11 @@ __device__ __forceinline__ int2 worker_info(const PagedView &v, const PagedPlan 
   return make_int2(p.row, p.first >= 0 ? p.first : worker_of_slot(p.start - (uint32_t)p.page, p));
 }
 
-// Rows without a cached token: zeros, and -inf for the log-sum-exp.  All warps of the grid call it (whole warps); row r belongs
-// to warp r % (their number), 32 rows looked at per load.
+// Rows without a cached token: zeros, and -inf for the log-sum-exp.  Whole warps call it, `mine` of `warps`; row r belongs to warp
+// r % warps, 32 rows looked at per load.
 template <typename T>
-__device__ __forceinline__ void zero_empty_rows(const PagedView &v, const PagedOut &o, int H, int Dv) {
-  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  const int64_t warps = (int64_t)gridDim.x * nw, mine = (int64_t)blockIdx.x * nw + (threadIdx.x >> 5);
+__device__ __forceinline__ void zero_empty_rows(const PagedView &v, const PagedOut &o, int H, int Dv, int64_t mine, int64_t warps) {
+  const int lane = threadIdx.x & 31;
   for (int64_t r0 = mine; r0 < v.T; r0 += 32 * warps) {
     const int64_t r = r0 + lane * warps;
     uint32_t empty = __ballot_sync(0xffffffffu, r < v.T && row_slots(v, (int)r) == 0);
