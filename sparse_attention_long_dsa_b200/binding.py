@@ -304,7 +304,7 @@ def _dense(what: str, dtype, *tensors):
 
 
 def _shape(t, shape: tuple, what: str):
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise DSAError(DSA_ERR_INVALID_ARG, what, f"shape {tuple(t.shape)}; expected {shape}")
 
 

@@ -24,13 +24,14 @@
 //              page's ninth block, half in one of two 4 KB buffers, so that two pages of it are in flight.
 // P is rounded to bf16 for P V, as the tensor cores take it (2^-8 of a weight); the sum l keeps the unrounded weights in fp32.
 //
-// Measured on one B200, the join included: 1 row of 1,048,576 tokens 280 us (4.3 TB/s of keys, 1.04 PFLOP/s) in short bursts,
-// 334 us in a loop of seconds, where the 1000 W cap holds the SM clock at 1.3 - 1.6 GHz; 32 rows of 4K - 32K tokens 137 us,
-// 165 us in a loop (the kernel alone 126 us: DRAM 56 %, tensor pipe 54 % busy); 61 rows up to 8K, 16 heads, 69 us.  A page
-// takes 1.2 us of a pair: 0.83 us is what DRAM gives, 1,425 cycles the matrix instructions (QK^T 36 steps of 25.3 cycles, held
-// by the operand reads at N = 64; P V 8 of 64.3), and what is left is the way of a buffer through copy, QK^T, softmax, P V.
-// What lost: QK^T of two pages as one N = 128 instruction (32.3 cycles a step, but a page then waits for the next one: 299 us,
-// 343 in a loop), the latent entries split over the pair with partial scores exchanged (831 us: 32 KB through distributed
+// Measured on one B200, the join included: 1 row of 1,048,576 tokens 264 - 275 us (4.5 TB/s of keys, 1.1 PFLOP/s) in short
+// bursts, 320 us in a loop of seconds, where the 1000 W cap holds the SM clock at 1.3 - 1.6 GHz; 32 rows of 4K - 32K tokens
+// 130 us, 157 us in a loop (DRAM 54 %, tensor pipe 53 % busy); 61 rows up to 8K, 16 heads, 68 us; 1 row of 130 tokens 11 us.
+// A page takes 1.2 us of a pair: 0.83 us is what DRAM gives, 1,425 cycles the matrix instructions (QK^T 36 steps of 25.3
+// cycles, held by the operand reads at N = 64; P V 8 of 64.3), and what is left is the way of a buffer through copy, QK^T,
+// softmax, P V.
+// What lost: QK^T of two pages as one N = 128 instruction (32.3 cycles a step, but a page then waits for the next one: 1M row
+// 280 -> 299 us), the latent entries split over the pair with partial scores exchanged (831 us: 32 KB through distributed
 // shared memory take 1,950 cycles), pages brought into L2 ahead of their copies (no gain with four buffers).
 #include <algorithm>
 #include <atomic>

@@ -106,8 +106,9 @@ struct PlanThreads {
 // The split by rows; thread r has row r, of `mine` slots behind `before` others.  c0, c1, c2: the longest pieces to try; c2 needs
 // at most W workers, the others at most 2 W; rows of at most `whole` slots stay whole.  false: a piece would be longer than `limit`.
 template <bool kWarp>
-__device__ __forceinline__ bool split_rows(const PlanThreads<kWarp> &th, int worker, uint32_t mine, uint32_t before, uint32_t total, uint32_t limit, uint32_t W,
-                                           uint32_t whole, uint32_t c0, uint32_t c1, uint32_t c2, PagedPlan *p) {
+__device__ __forceinline__ bool split_rows(const PlanThreads<kWarp> &th, int worker, uint32_t mine, uint32_t before, uint32_t total,
+                                           uint32_t limit, uint32_t W, uint32_t whole, uint32_t c0, uint32_t c1, uint32_t c2,
+                                           PagedPlan *p) {
   // 10 bits for each count of workers: W <= 148
   uint32_t n0 = (mine + c0 - 1) / c0, n1 = (mine + c1 - 1) / c1, n2 = (mine + c2 - 1) / c2;
   if (mine <= whole) n0 = n1 = n2 = min(mine, 1u);

@@ -867,6 +867,50 @@ def test_a_captured_step_replays_as_the_cache_grows():
             _view(cache, heads).check(q, 0.07, out, lse)
 
 
+def test_two_captured_steps_of_one_cache_take_turns():
+    """A decode step and a step of 40-row chunks, captured one after the other: they share the workspace, the tables and the
+    descriptors, and are replayed in any order, padding rows among theirs."""
+    n, heads = 3, 5
+    cache = PagedCache(n, 60, 20, heads)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(8)
+    w, freq = torch.ones(512, device=DEV), torch.tensor(_freq(64), device=DEV)
+    q = torch.randn((n, heads, 576), generator=g, device=DEV).bfloat16()
+    out, lse = torch.empty((n, heads, 512), dtype=torch.bfloat16, device=DEV), torch.empty((n, heads), device=DEV)
+    new = {3: _i32([0, 0, 0]), 40: _i32([0, 0, 0])}
+    kv = {t: torch.zeros((t, 576), dtype=torch.bfloat16, device=DEV) for t in new}
+
+    def step(t):
+        cache.extend(new[t], t)
+        cache.store(kv[t], w, freq)
+        cache.attend(q, out, 0.07, lse=lse)
+
+    graphs = {}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for t in new:
+            step(t)
+    torch.cuda.current_stream().wait_stream(side)
+    for t in new:
+        graphs[t] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[t]):
+            step(t)
+    want, rng = np.zeros(3, dtype=np.int64), np.random.default_rng(8)
+    for i in range(30):
+        t = 40 if rng.random() < 0.4 else 3
+        add = rng.multinomial(rng.integers(0, t + 1), [0.5, 0.3, 0.2]) if t == 40 else rng.integers(0, 2, 3)
+        new[t].copy_(_i32(add))
+        kv[t].copy_(torch.randn((t, 576), generator=g, device=DEV))
+        graphs[t].replay()
+        want += add
+        if i % 7 == 6 or i == 29:
+            cache.check_status()
+            assert cache.seq_lens.tolist() == want.tolist()
+            assert cache.free_count.item() == 60 - int(sum(-(-want // 64)))
+            _view(cache, heads).check(q, 0.07, out, lse)
+
+
 def test_steps_of_many_sizes_share_buffers_and_keep_their_addresses():
     cache = PagedCache(2, 40, 30, 4)
     seen, total = {}, 0
