@@ -158,10 +158,11 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device: Optional[int] = None) -> Optional[int]:
+    """A stream's handle; None: the current stream of the current device (device, where the caller knows it)."""
     if stream is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -293,14 +294,16 @@ def dsa_cp_merge(part_out, dt: int, part_lse, G: int, T: int, H: int, Dv: int, o
 def _dense(what: str, dtype, *tensors):
     """Addresses of dense tensors of one dtype on the current device."""
     import torch
-    cur = torch._C._cuda_getDevice() if tensors[0].is_cuda else -1
+    dev = tensors[0].get_device()
+    cur = torch._C._cuda_getDevice() if dev >= 0 else -2
+    at = [t.data_ptr() for t in tensors if t.dtype is dtype and t.get_device() == cur and t.is_contiguous()]
+    if len(at) == len(tensors):
+        return at
     for t in tensors:
         if t.dtype is not dtype:
             raise DSAError(DSA_ERR_INVALID_ARG, what, f"a {t.dtype} tensor; expected {dtype}")
-        if t.get_device() != cur or cur < 0 or not t.is_contiguous():
-            _ptr(t)                                  # names a host or strided tensor
-            raise DSAError(DSA_ERR_INVALID_ARG, what, f"a tensor on {t.device}; the current device is cuda:{cur}")
-    return [t.data_ptr() for t in tensors]
+        _ptr(t)                                      # names a host or strided tensor
+    raise DSAError(DSA_ERR_INVALID_ARG, what, f"a tensor on another device than the current one, cuda:{torch.cuda.current_device()}")
 
 
 def _shape(t, shape: tuple, what: str):
@@ -321,18 +324,18 @@ def dsa_batch_extend(cached_lens, new_lens, page_size: int, num_blocks: int, tot
     and free_left may be free_count."""
     import torch
     w = "dsa_batch_extend"
-    n = cached_lens.numel()
-    _shape(new_lens, (n,), w)
-    _shape(seq_lens, (n,), w)
-    _shape(cu_q, (n + 1,), w)
-    if block_table.dim() != 2 or block_table.shape[0] != n or slots.numel() < total_q or positions.numel() < total_q:
+    n, table_shape = cached_lens.numel(), block_table.shape
+    if new_lens.shape != (n,) or seq_lens.shape != (n,) or cu_q.shape != (n + 1,):
+        raise DSAError(DSA_ERR_INVALID_ARG, w, f"new_lens {tuple(new_lens.shape)}, seq_lens {tuple(seq_lens.shape)}, cu_q "
+                       f"{tuple(cu_q.shape)}; expected ({n},), ({n},), ({n + 1},)")
+    if len(table_shape) != 2 or table_shape[0] != n or slots.numel() < total_q or positions.numel() < total_q:
         raise DSAError(DSA_ERR_INVALID_ARG, w, f"block_table [{n}, max_blocks], slots and positions [total_q] expected")
     cached, new, free, count, table, seq, cu, pos, left = _dense(w, torch.int32, cached_lens, new_lens, free_blocks, free_count,
                                                                  block_table, seq_lens, cu_q, positions, free_left)
     slot, = _dense(w, torch.int64, slots)
-    _check((_lib or load()).dsa_batch_extend(cached, new, n, page_size, block_table.shape[1], num_blocks, total_q, free,
+    _check((_lib or load()).dsa_batch_extend(cached, new, n, page_size, table_shape[1], num_blocks, total_q, free,
                                              free_blocks.numel(), count, table, seq, cu, slot, pos, left, _ptr(ws), ws_bytes,
-                                             _stream(stream)), w)
+                                             _stream(stream, cached_lens.get_device())), w)
 
 
 def dsa_batch_release(done, page_size: int, num_blocks: int, block_table, seq_lens, free_blocks, free_count, ws,
@@ -347,6 +350,9 @@ def dsa_batch_release(done, page_size: int, num_blocks: int, block_table, seq_le
     d, table, seq, free, count = _dense(w, torch.int32, done, block_table, seq_lens, free_blocks, free_count)
     _check((_lib or load()).dsa_batch_release(d, n, page_size, block_table.shape[1], num_blocks, table, seq, free,
                                               free_blocks.numel(), count, _ptr(ws), ws_bytes, _stream(stream)), w)
+
+
+_PARTS = tuple(dsa_rope_part_t * n for n in range(5))
 
 
 def rope_part(x, out, *, weight=None, norm=(0, 0), eps: float = 1e-6, rope=(0, 0), style: str = "pairs", slots=None,
@@ -400,6 +406,7 @@ def rope_part(x, out, *, weight=None, norm=(0, 0), eps: float = 1e-6, rope=(0, 0
                            rope_style=DSA_ROPE_HALVES if style == "halves" else DSA_ROPE_PAIRS, eps=eps)
     part.rows = T
     part.device = x.get_device()
+    part.rotated = rope[1]
     part.tensors = (x, out, weight, scale, slots)
     return part
 
@@ -412,19 +419,20 @@ def dsa_qk_norm_rope(parts, positions, inv_freq, ws, ws_bytes: int, stream=None)
     if not 1 <= len(parts) <= 4:
         raise DSAError(DSA_ERR_UNSUPPORTED, w, f"{len(parts)} parts; 1 to 4 are taken")
     T, cur = parts[0].rows, torch._C._cuda_getDevice()       # the parts hold CUDA tensors: CUDA is up
+    half = None if inv_freq is None else inv_freq.numel()
     for p in parts:
         if p.rows != T:
             raise DSAError(DSA_ERR_INVALID_ARG, w, f"parts of {T} and {p.rows} rows")
         if p.device != cur:
             raise DSAError(DSA_ERR_INVALID_ARG, w, f"a part on cuda:{p.device}; the current device is cuda:{cur}")
-        if inv_freq is not None and p.rope_len and inv_freq.numel() != p.rope_len // 2:
-            raise DSAError(DSA_ERR_INVALID_ARG, w, f"{inv_freq.numel()} frequencies for rope_len {p.rope_len}")
+        if half is not None and p.rotated and half != p.rotated // 2:
+            raise DSAError(DSA_ERR_INVALID_ARG, w, f"{half} frequencies for rope_len {p.rotated}")
     if positions is not None:
         _shape(positions, (T,), w)
     pos = None if positions is None else _dense(w, torch.int32, positions)[0]
     freq = None if inv_freq is None else _dense(w, torch.float64, inv_freq)[0]
-    arr = (dsa_rope_part_t * len(parts))(*parts)
-    _check((_lib or load()).dsa_qk_norm_rope(arr, len(parts), pos, T, freq, _ptr(ws), ws_bytes, _stream(stream)), w)
+    arr = _PARTS[len(parts)](*parts)
+    _check((_lib or load()).dsa_qk_norm_rope(arr, len(parts), pos, T, freq, _ptr(ws), ws_bytes, _stream(stream, cur)), w)
 
 
 def page_list_width(pages, rows: int) -> int:
