@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a) 
   }
   pdl_wait();
   pdl_trigger();
-  plan_pages(a.view, worker, gridDim.x, 1, 1, S.tmp, &S.plan);       // one row of 8 pages 7.3 us, 9.0 with two pages per worker
+  plan_pages(a.view, worker, gridDim.x, 1, 1, 1, S.tmp, &S.plan);       // one row of 8 pages 7.3 us, 9.0 with two pages per worker
   if (tid == 0) a.o.info[worker] = worker_info(a.view, S.plan);
 
   SegmentWalk walk(S.plan);

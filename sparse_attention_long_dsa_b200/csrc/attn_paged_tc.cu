@@ -49,6 +49,10 @@ constexpr int kPtRing = 8;                         // published pages in flight
 // pages 13.0 us whole, 14.3 in two pieces; 16 rows of 5 pages 14.6, 16.7; one row of 8 pages 14.5 us in pieces of two, 16.0 of
 // four; of 128 pages 20.4 in pieces of two, 19.2 of four (one row of 64 times min_slots takes twice as many).
 constexpr uint32_t kPtMinSlots = 2, kPtWhole = 5;
+// The longest row that stays whole when there are more rows than workers, for more heads than 32 and for up to 32 (the results and
+// q of a segment count less then).  128 heads: 128 rows of 8 pages 31.8 us, 40.4 cut anywhere; 100 rows of 8 - 13 pages 35.5, 40.8.  16 heads: 128 rows of
+// 2 - 7 pages 22.8, 25.9; 80 rows of 11 - 16 pages cut anywhere 30.4, 36.2 whole.
+constexpr uint32_t kPtUncutMany = 16, kPtUncutFew = 10;
 constexpr int kPtThreads = 384;                    // softmax x 8, keys, QK^T, P V, values
 constexpr int kPtGroup = 128;                      // threads of a softmax group (4 warps)
 constexpr int kPtWarpKeys = 8, kPtWarpQK = 9, kPtWarpPV = 10, kPtWarpValues = 11;
@@ -220,7 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
   // inputs come from earlier work on the stream
   pdl_wait();
   pdl_trigger();
-  plan_pages(a.view, pair, npairs, kPtMinSlots, kPtWhole, S->tmp, &S->plan);
+  plan_pages(a.view, pair, npairs, kPtMinSlots, kPtWhole, a.H > 32 ? kPtUncutMany : kPtUncutFew, S->tmp, &S->plan);
 
   // next entry of the ring, for a whole warp: false ends the role (the end of the work, or a wait that ran out)
   auto next_entry = [&](uint32_t &ec, int4 *e) -> bool {

@@ -135,7 +135,7 @@ __device__ __forceinline__ bool split_rows(const PlanThreads<kWarp> &th, int wor
 
 template <bool kWarp>
 __device__ __forceinline__ void make_plan(const PlanThreads<kWarp> &th, const PagedView &v, int worker, int workers,
-                                          uint32_t min_slots, uint32_t whole, PagedPlan *p) {
+                                          uint32_t min_slots, uint32_t whole, uint32_t uncut, PagedPlan *p) {
   const int nt = th.count(), per = kWarp ? 1 : (v.T + nt - 1) / nt;
   const int r0 = min(v.T, (int)threadIdx.x * per), r1 = min(v.T, r0 + per);
   uint32_t mine = 0;
@@ -155,10 +155,12 @@ __device__ __forceinline__ void make_plan(const PlanThreads<kWarp> &th, const Pa
   // rows of one page or none 11.9, 15.3; 16 rows of 1 - 13 pages 18.0, 20.7.  f32: 16 rows of 4 - 128 pages, 4 heads of 64 13.2,
   // 13.9; 16 heads of 128 33.6, 38.4.  Where it turns out not to pay, looking for it costs 0.3 us.
   constexpr uint32_t kSegment = 4;
+  uint32_t keep = whole;
   if (v.T > 1) {
     const uint32_t n0 = total / (uint32_t)v.T;
     const bool same = th.all(mine == n0 * (uint32_t)(r1 - r0));
     const int rows = same ? v.T : th.that(mine > 0);
+    if (rows > workers) keep = uncut;                  // no worker to spare for a piece of a row
     const uint32_t limit = total / (uint32_t)np + kSegment;
     if (same && rows <= workers) {
       const uint32_t each = rows < np && n0 > whole ? (uint32_t)np / (uint32_t)rows : 1u;
@@ -183,8 +185,8 @@ __device__ __forceinline__ void make_plan(const PlanThreads<kWarp> &th, const Pa
     if (start >= end) p->start = total;
     if (start >= end || end == total) p->end = total;
   }
-  // The threads whose rows the two borders lie in.  A border inside a row that stays whole moves to the nearer end of it: 250 rows
-  // of one or two pages, 64 heads, 23.1 us, 26.8 cut where they are; 100 of 2 to 7 pages 26.1, 28.8.
+  // The threads whose rows the two borders lie in.  A border inside a row of at most `keep` slots moves to the nearer end of it: a
+  // cut costs a segment, partial results and their join.
   if (start < end) {
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
@@ -199,7 +201,7 @@ __device__ __forceinline__ void make_plan(const PlanThreads<kWarp> &th, const Pa
             at += n;
           }
         uint32_t page = x - at;
-        if (page > 0 && n <= whole) {
+        if (page > 0 && n <= keep) {
           if (2 * page >= n) {
             at += n;
             ++r;
@@ -220,9 +222,9 @@ __device__ __forceinline__ void make_plan(const PlanThreads<kWarp> &th, const Pa
 
 // Every thread of the block calls this (blockDim.x a multiple of 32, at most 1024); `tmp` holds 33 words.
 __device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int workers, uint32_t min_slots, uint32_t whole,
-                                           uint32_t *tmp, PagedPlan *p) {
-  if (v.T > 32) make_plan(PlanThreads<false>{tmp}, v, worker, workers, min_slots, whole, p);
-  else if (threadIdx.x < 32) make_plan(PlanThreads<true>{tmp}, v, worker, workers, min_slots, whole, p);
+                                           uint32_t uncut, uint32_t *tmp, PagedPlan *p) {
+  if (v.T > 32) make_plan(PlanThreads<false>{tmp}, v, worker, workers, min_slots, whole, uncut, p);
+  else if (threadIdx.x < 32) make_plan(PlanThreads<true>{tmp}, v, worker, workers, min_slots, whole, uncut, p);
   __syncthreads();
 }
 

@@ -625,7 +625,7 @@ def test_same_bits_again_without_lse_on_other_streams_and_with_two_calls_at_once
 @pytest.mark.parametrize("rows,lo,hi,empty", [
     (2, 16, 33, 0), (3, 100, 400, 0), (8, 87, 175, 0), (16, 0, 794, 0), (26, 1, 54, 9), (74, 1, 60, 0), (75, 1, 60, 1),
     (75, 1, 60, 0), (148, 64, 130, 0), (200, 1, 400, 150), (300, 1, 3000, 270), (390, 1, 90, 350), (6, 1035, 2070, 1),
-    (40, 1, 900, 0), (30, 60, 70, 0),
+    (40, 1, 900, 0), (30, 60, 70, 0), (100, 300, 1100, 0), (80, 700, 1000, 3), (160, 1, 640, 5), (128, 512, 512, 0), (151, 65, 800, 2),
 ])
 def test_batches_of_rows_of_different_lengths(heads, f32, rows, lo, hi, empty):
     """Small batches are cut into pieces of rows, others into equal ranges of pages: both sides, and where they meet."""
