@@ -106,7 +106,9 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a) 
   }
   pdl_wait();
   pdl_trigger();
-  plan_pages(a.view, worker, gridDim.x, 1, 1, 1, S.tmp, &S.plan);       // one row of 8 pages 7.3 us, 9.0 with two pages per worker
+  // One row of 8 pages: 7.3 us with a page per worker, 9.0 with two.  More rows than workers, none of up to 8 pages cut: 220 rows of
+  // 1 - 3 pages, 13 heads of 32 17.8 us, 25.9 cut anywhere; 150 of 2 - 7 pages 15.1, 16.5; 160 of 5 pages 19.5, 17.8.
+  plan_pages(a.view, worker, gridDim.x, 1, 1, 8, S.tmp, &S.plan);
   if (tid == 0) a.o.info[worker] = worker_info(a.view, S.plan);
 
   SegmentWalk walk(S.plan);
