@@ -24,9 +24,9 @@
 //              page's ninth block, half in one of two 4 KB buffers, so that two pages of it are in flight.
 // P is rounded to bf16 for P V, as the tensor cores take it (2^-8 of a weight); the sum l keeps the unrounded weights in fp32.
 //
-// Measured on one B200, the join included: 1 row of 1,048,576 tokens 264 - 275 us (4.5 TB/s of keys, 1.1 PFLOP/s) in short
-// bursts, 320 us in a loop of seconds, where the 1000 W cap holds the SM clock at 1.3 - 1.6 GHz; 32 rows of 4K - 32K tokens
-// 130 us, 157 us in a loop (DRAM 54 %, tensor pipe 53 % busy); 61 rows up to 8K, 16 heads, 68 us; 1 row of 130 tokens 11 us.
+// Measured on one B200, the join included: 1 row of 1,048,576 tokens 261 - 275 us (4.5 TB/s of keys, 1.1 PFLOP/s) in short
+// bursts, 314 us in a loop of seconds, where the 1000 W cap holds the SM clock at 1.3 - 1.6 GHz; 32 rows of 4K - 32K tokens
+// 129 us, 155 us in a loop (DRAM 54 %, tensor pipe 53 % busy); 61 rows up to 8K, 16 heads, 68 us; 1 row of 130 tokens 11 us.
 // A page takes 1.2 us of a pair: 0.83 us is what DRAM gives, 1,425 cycles the matrix instructions (QK^T 36 steps of 25.3
 // cycles, held by the operand reads at N = 64; P V 8 of 64.3), and what is left is the way of a buffer through copy, QK^T,
 // softmax, P V.
