@@ -5,14 +5,14 @@
 // Practices for Day-0 Adaptation of Million-Token Context Models on Domestic AI Chips", Four Key Layers 3: the decode
 // unit walks the KV blocks and the partial results are merged by a cross-block reduction).
 //
-// The f32 path: a CTA takes a range of page slots (paged.cuh) and its 8 warps take batches of 8 to 32 tokens of it in turn.
+// The f32 path: a CTA takes a range of page slots (paged.cuh) and its 8 or 12 warps take batches of 8 to 32 tokens of it in turn.
 // LT lanes stand over a token's entries, four each, so keys and values go from HBM to registers in whole rows, eight keys and
 // eight values per lane in flight; a lane holds its four entries of every head's q and output.  The partial dot products of
 // HP heads are summed over the LT lanes by halving exchanges (each step halves the values a lane carries: HP - 1 shuffles
 // instead of HP log2(LT)), which leaves each (token, head) in one lane for the softmax; the weights come back through a
 // warp's own shared memory.  Warps are joined at the end of a segment, in their order.  Tokens past the sequence are not
 // loaded: what the cache holds there may be anything.
-// Bound by the issue of loads, FMAs and shuffles from two warps per scheduler (q, output, keys and values of a batch take most
+// Bound by the issue of loads, FMAs and shuffles from two or three warps per scheduler (q, output, keys and values of a batch take most
 // of the registers).  16 rows of 256 - 8,192 tokens (61,000 in all, 31 MB at 4 heads of 64): 13 us, the bytes alone 4.8 us;
 // 16 heads of 64: 23 us, 16 heads of 128 (64 MB): 34 us; one row of 131,072 tokens, 4 heads of 64: 20 us (67 MB, 3.3 TB/s).
 // Two CTAs per SM with half the registers, and the next batch's keys loaded a batch ahead, were both slower.
@@ -25,7 +25,6 @@ namespace dsa {
 dsa_status_t paged_mla_launch(const void *q, const void *kv, int H, float softmax_scale, const PagedView &view,
                               const PagedOut &o, int max_workers, cudaStream_t stream, int num_sms, int *workers);
 
-constexpr int kPsThreads = 256, kPsWarps = kPsThreads / 32;
 constexpr int kPsSteps = 8;                        // keys (and values) of a lane in flight
 
 struct PsArgs {
@@ -74,19 +73,19 @@ __device__ __forceinline__ void ps_reduce(float (&z)[HP], int lane) {
   }
 }
 
-template <int LT, int HP>
+template <int LT, int HP, int NW>
 struct PsSmem {
   static constexpr int kTok = 32 / LT * kPsSteps;  // tokens of a batch
-  float p[kPsWarps][kTok][HP];
-  float alpha[kPsWarps][HP], m[kPsWarps][HP], l[kPsWarps][HP];
-  float o[kPsWarps][HP][4 * LT];
+  float p[NW][kTok][HP];
+  float alpha[NW][HP], m[NW][HP], l[NW][HP];
+  float o[NW][HP][4 * LT];
   uint32_t tmp[33];
   PagedPlan plan;
 };
 
-template <int LT, int HP>
-__global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a) {
-  using Smem = PsSmem<LT, HP>;
+template <int LT, int HP, int NW>
+__global__ void __launch_bounds__(32 * NW) paged_simt_kernel(const PsArgs a) {
+  using Smem = PsSmem<LT, HP, NW>;
   constexpr int TW = 32 / LT, kTok = Smem::kTok, HV = HP > LT ? HP / LT : 1;
   extern __shared__ float4 sm4[];
   Smem &S = *reinterpret_cast<Smem *>(sm4);
@@ -132,7 +131,7 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a) 
       l[i] = 0.f;
     }
     constexpr int kPer = kPage / kTok;             // batches of a page
-    for (int u = sa * kPer + warp; u < sb * kPer; u += kPsWarps) {
+    for (int u = sa * kPer + warp; u < sb * kPer; u += NW) {
       int blk = 0;
       const int t0 = (u % kPer) * kTok, ntok = slot_tokens(a.view, row, n, u / kPer, &blk, a.o.status) - t0;
       if (ntok <= 0) continue;                     // the same for the whole warp
@@ -244,14 +243,14 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a) 
       S.l[warp][first + i] = l[i];
     }
     __syncthreads();
-    for (int i = tid; i < H * Dv; i += kPsThreads) {
+    for (int i = tid; i < H * Dv; i += 32 * NW) {
       const int h = i / Dv, d = i - h * Dv;
       float M = -INFINITY, L = 0.f, acc = 0.f;
 #pragma unroll
-      for (int w = 0; w < kPsWarps; ++w) M = fmaxf(M, S.m[w][h]);
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, S.m[w][h]);
       const float use = M == -INFINITY ? 0.f : M;
 #pragma unroll
-      for (int w = 0; w < kPsWarps; ++w) {
+      for (int w = 0; w < NW; ++w) {
         const float e = exp2f(S.m[w][h] - use);
         L = fmaf(e, S.l[w][h], L);
         acc = fmaf(e, S.o[w][h][d], acc);
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(kPsThreads) paged_simt_kernel(const PsArgs a) 
     }
     __syncthreads();
   }
-  zero_empty_rows<float>(a.view, a.o, H, Dv, (int64_t)blockIdx.x * kPsWarps + warp, (int64_t)gridDim.x * kPsWarps);
+  zero_empty_rows<float>(a.view, a.o, H, Dv, (int64_t)blockIdx.x * NW + warp, (int64_t)gridDim.x * NW);
 }
 
 // ------------------------------------------------------------------------------------------------ join
@@ -438,22 +437,26 @@ static PagedOut paged_out(void *ws, int H, int Dv, void *out, float *lse) {
   return o;
 }
 
-template <int LT, int HP>
+template <int LT, int HP, int NW>
 static dsa_status_t simt_launch(const PsArgs &a, int workers, cudaStream_t stream) {
-  auto *k = paged_simt_kernel<LT, HP>;
-  constexpr size_t smem = sizeof(PsSmem<LT, HP>);
+  auto *k = paged_simt_kernel<LT, HP, NW>;
+  constexpr size_t smem = sizeof(PsSmem<LT, HP, NW>);
   if (smem > 48 * 1024 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     set_error("paged_simt_kernel: %s", cudaGetErrorString(cudaGetLastError()));
     return DSA_ERR_CUDA;
   }
-  DSA_LAUNCH_PDL("paged_simt_kernel", k, dim3(workers), dim3(kPsThreads), smem, stream, a);
+  DSA_LAUNCH_PDL("paged_simt_kernel", k, dim3(workers), dim3(32 * NW), smem, stream, a);
   return DSA_OK;
 }
+// 8 warps of up to 255 registers.  Up to 4 heads 128 are enough, so 12 warps run where every CTA has rows of its own: 256 rows of 8 -
+// 13 pages 24.7 us, 32.2 with 8 warps, 180 of 11 - 24 pages, 128 entries wide 46.7, 60.8; but one row of 2 pages 7.3, 6.8, one of
+// 131,072 tokens 22.5, 19.6.
 template <int LT>
 static dsa_status_t simt_heads(const PsArgs &a, int workers, cudaStream_t stream) {
-  if (a.H <= 4) return simt_launch<LT, 4>(a, workers, stream);
-  if (a.H <= 8) return simt_launch<LT, 8>(a, workers, stream);
-  return simt_launch<LT, 16>(a, workers, stream);
+  if (a.H <= 4 && a.view.T > workers) return simt_launch<LT, 4, 12>(a, workers, stream);
+  if (a.H <= 4) return simt_launch<LT, 4, 8>(a, workers, stream);
+  if (a.H <= 8) return simt_launch<LT, 8, 8>(a, workers, stream);
+  return simt_launch<LT, 16, 8>(a, workers, stream);
 }
 
 dsa_status_t paged_attn_launch(const void *q, bool bf16, const void *kv, const void *v, int H, int Dqk, int Dv,

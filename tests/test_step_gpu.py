@@ -639,6 +639,17 @@ def test_batches_of_rows_of_different_lengths(heads, f32, rows, lo, hi, empty):
     c.check(q, 0.07, out, lse)
 
 
+@pytest.mark.parametrize("heads,dqk,dv", [(1, 32, 32), (4, 20, 32), (3, 61, 64), (4, 128, 100), (2, 7, 5)])
+@pytest.mark.parametrize("rows,hi", [(148, 500), (149, 500), (300, 40), (250, 1000)])
+def test_f32_batches_around_the_number_of_workers(heads, dqk, dv, rows, hi):
+    rng = np.random.default_rng(rows + heads)
+    c = _Cache(rng.integers(0, hi + 1, rows).tolist(), f32=(dqk, dv), seed=rows)
+    q = c.q(heads)
+    out, lse = c.attend(q, dqk ** -0.5)
+    B.dsa_read_device_status(c.ws)
+    c.check(q, dqk ** -0.5, out, lse)
+
+
 @pytest.mark.parametrize("heads,f32", [(128, None), (4, (64, 64))])
 def test_a_head_that_is_nan_stays_nan_and_alone(heads, f32):
     """A NaN in one head's query: NaN in its result and its log-sum-exp, whether the row is split or not; the other heads keep
