@@ -51,7 +51,11 @@
  *   cu_q[b] .. cu_q[b+1]-1, which are its LAST n_b = cu_q[b+1]-cu_q[b] tokens:
  *   row cu_q[b]+i sits at absolute position pos = seq_lens[b] - n_b + i and may
  *   attend to positions 0..pos (its own entry is already in the cache).
- *   A sequence may own no rows (n_b == 0) anywhere in the batch.  An empty batch
+ *   A sequence may own no rows (n_b == 0) anywhere in the batch.  Rows at or past cu_q[num_seqs]
+ *   (padding of a captured step: total_q is then a capacity) belong to no sequence: nothing is scored or
+ *   appended for them and their selections are all -1, so that attention gives zeros and an lse of -inf.
+ *   A sequence without cached tokens may own one row, with the same results (only appending it is an
+ *   error); its first block_table entry must still name a block.  An empty batch
  *   (total_q == 0) is a no-op: every compute call checks the descriptor and returns
  *   DSA_OK without enqueueing anything or needing a device; its data pointers may
  *   then be NULL.
@@ -109,8 +113,9 @@ typedef enum {
 
 /* Batch descriptor shared by every call.  The three host integers at the end are
  * upper bounds the caller already knows; they size grids without a device->host
- * read.  They must hold: total_q == cu_q[num_seqs], max_q_per_seq >= every n_b,
- * max_seq_len >= every seq_lens[b]. */
+ * read.  They must hold: total_q >= cu_q[num_seqs] (rows behind it belong to no sequence),
+ * max_q_per_seq >= every n_b, max_seq_len >= every seq_lens[b].  total_q == num_seqs with max_q_per_seq == 1 says
+ * more: a decode batch, cu_q[b] == b. */
 typedef struct {
   int32_t num_seqs;            /* B >= 1 */
   int32_t page_size;           /* tokens per block: 64 */
@@ -119,7 +124,7 @@ typedef struct {
   const int32_t *block_table;  /* device [num_seqs, max_blocks_per_seq], values in [0, num_blocks) */
   const int32_t *seq_lens;     /* device [num_seqs], cached tokens including the query rows' own */
   const int32_t *cu_q;         /* device [num_seqs + 1], cu_q[0] = 0, non-decreasing */
-  int32_t total_q;             /* host: cu_q[num_seqs] */
+  int32_t total_q;             /* host: >= cu_q[num_seqs] */
   int32_t max_q_per_seq;       /* host: >= max_b (cu_q[b+1] - cu_q[b]) */
   int32_t max_seq_len;         /* host: >= max_b seq_lens[b] */
 } dsa_batch_t;

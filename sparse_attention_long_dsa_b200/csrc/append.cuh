@@ -47,7 +47,8 @@ __device__ __forceinline__ void append_token_warp(const AppendArgs &a, const Bat
   int b;
   const int pos = pos_of_row_warp(bv, row, &b);
   if (pos < 0 || pos >= bv.max_blocks_per_seq * bv.page_size) {
-    if (lane == 0) set_status(status, kStatusBadIndex);
+    // a row of no sequence is no token; any other one is an error
+    if (lane == 0 && row < __ldg(bv.cu_q + bv.num_seqs)) set_status(status, kStatusBadIndex);
     return;
   }
   const int64_t pr = phys_row(bv, b, pos);

@@ -48,12 +48,14 @@ __device__ __forceinline__ int seq_of_row(const int32_t *cu_q, int num_seqs, int
   return lo;
 }
 
-// absolute position of a query row: rows of sequence b are its last n_b tokens
+// Absolute position of a query row: rows [c0, c1) of a sequence of n tokens are its last c1 - c0.  -1, so that nothing is
+// causal, for a row at or past cu_q[num_seqs]: the searches below give it the last sequence, whose rows end before it.
+__device__ __forceinline__ int row_pos(int row, int c0, int c1, int n) { return row < c1 ? n - (c1 - c0) + (row - c0) : -1; }
 __device__ __forceinline__ int pos_of_row(const BatchView &bv, int row, int *seq_out) {
   int b = seq_of_row(bv.cu_q, bv.num_seqs, row);
   int c0 = __ldg(bv.cu_q + b), c1 = __ldg(bv.cu_q + b + 1);
   *seq_out = b;
-  return __ldg(bv.seq_lens + b) - (c1 - c0) + (row - c0);
+  return row_pos(row, c0, c1, __ldg(bv.seq_lens + b));
 }
 
 // seq_of_row for a whole warp (every lane calls it with the same row and gets the same result): each
@@ -82,7 +84,7 @@ __device__ __forceinline__ int pos_of_row_warp(const BatchView &bv, int row, int
   int b = seq_of_row_warp(bv.cu_q, bv.num_seqs, row);
   int c0 = __ldg(bv.cu_q + b), c1 = __ldg(bv.cu_q + b + 1);
   *seq_out = b;
-  return __ldg(bv.seq_lens + b) - (c1 - c0) + (row - c0);
+  return row_pos(row, c0, c1, __ldg(bv.seq_lens + b));
 }
 
 // physical row (block * page + slot) of logical token s of sequence b; -1 if the block id is bad

@@ -241,9 +241,8 @@ __device__ __forceinline__ int sel_row_len(const BatchView &bv, int row) {
     ssl = __ldg(bv.seq_lens + row);
   }
   const int b = seq_of_row_warp(bv.cu_q, bv.num_seqs, row);
-  if (b == row) return ssl - (sc1 - sc0) + (row - sc0) + 1;
-  const int c0 = __ldg(bv.cu_q + b), c1 = __ldg(bv.cu_q + b + 1);
-  return __ldg(bv.seq_lens + b) - (c1 - c0) + (row - c0) + 1;
+  if (b == row) return row_pos(row, sc0, sc1, ssl) + 1;
+  return row_pos(row, __ldg(bv.cu_q + b), __ldg(bv.cu_q + b + 1), __ldg(bv.seq_lens + b)) + 1;
 }
 
 struct GatherArgs {
@@ -344,23 +343,7 @@ __global__ void __launch_bounds__(kSelThreads, kGathered ? 1 : 2) select_stream_
   const uint32_t C = sel_cl_nranks(), r = tc::cluster_ctarank();
   const int row = blockIdx.x / (int)C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the row's length: one round of loads for a batch of one query row per sequence (the row is its sequence)
-  int n;
-  {
-    int sc0 = 0, sc1 = 0, ssl = 0;
-    if (row < a.bv.num_seqs) {
-      sc0 = __ldg(a.bv.cu_q + row);
-      sc1 = __ldg(a.bv.cu_q + row + 1);
-      ssl = __ldg(a.bv.seq_lens + row);
-    }
-    const int b = seq_of_row_warp(a.bv.cu_q, a.bv.num_seqs, row);
-    if (b == row) {
-      n = ssl - (sc1 - sc0) + (row - sc0) + 1;
-    } else {
-      const int c0 = __ldg(a.bv.cu_q + b), c1 = __ldg(a.bv.cu_q + b + 1);
-      n = __ldg(a.bv.seq_lens + b) - (c1 - c0) + (row - c0) + 1;
-    }
-  }
+  const int n = sel_row_len(a.bv, row);
   int32_t *out = a.idx + (int64_t)row * a.k;
   // (every branch on n, on the row histograms and on the selection state is taken by the whole cluster)
   if (n <= a.k) {

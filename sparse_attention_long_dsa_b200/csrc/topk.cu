@@ -252,10 +252,9 @@ topk_rows_smem_kernel(const float *__restrict__ scores, int64_t ld, BatchView bv
     }
     const int b = seq_of_row_warp(bv.cu_q, bv.num_seqs, row);
     if (b == row) {
-      n = ssl - (sc1 - sc0) + (row - sc0) + 1;
+      n = row_pos(row, sc0, sc1, ssl) + 1;
     } else {
-      const int c0 = __ldg(bv.cu_q + b), c1 = __ldg(bv.cu_q + b + 1);
-      n = __ldg(bv.seq_lens + b) - (c1 - c0) + (row - c0) + 1;
+      n = row_pos(row, __ldg(bv.cu_q + b), __ldg(bv.cu_q + b + 1), __ldg(bv.seq_lens + b)) + 1;
     }
   }
   int32_t *out = idx + (int64_t)row * k;
