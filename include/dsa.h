@@ -346,8 +346,8 @@ DSA_API dsa_status_t dsa_cp_merge(const void *part_out, dsa_dtype_t dt, const fl
  *   seq_lens may be cached_lens itself and free_left may be free_count; no other arguments may overlap.
  *   A step that does not fit (a negative length, a sequence longer than its table row, more rows than total_q,
  *   fewer free blocks than needed, a count outside [0, free_capacity]) is refused as a whole: the table and the
- *   stack stay as they were, seq_lens holds the cached lengths (cut to [0, 64 max_blocks_per_seq]), cu_q follows
- *   the lengths (cut to total_q), every slot and position is -1, and dsa_read_device_status reports
+ *   stack stay as they were, seq_lens holds the cached lengths (cut to [0, 64 max_blocks_per_seq]), cu_q is all 0
+ *   (every row belongs to no sequence), every slot and position is -1, and dsa_read_device_status reports
  *   DSA_ERR_DEVICE_CHECK.  A block id outside [0, num_blocks), on the stack or in an entry that a row needs, is
  *   reported the same way; rows in that page get slot -1 (and the entry, if new, -1).
  * dsa_batch_release: sequences with done[b] != 0 give their ceil(seq_lens[b] / 64) blocks back, sequences in

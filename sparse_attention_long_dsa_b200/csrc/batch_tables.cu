@@ -114,8 +114,11 @@ __device__ __forceinline__ void extend_plan(const ExtendArgs &a) {
   bad = __syncthreads_or(bad);
   const bool refused = bad || rows > a.total_q || count < 0 || count > a.free_cap || need > count;
   // seq_lens may be the array `cached` itself: every entry of it has been read by now
-  for (int b = threadIdx.x; b < a.num_seqs; b += blockDim.x)
+  for (int b = threadIdx.x; b < a.num_seqs; b += blockDim.x) {
     a.seq_lens[b] = a.ws_cached[b] + (refused ? 0 : a.add[b]);
+    // no rows: cached lengths with the refused rows would put rows at negative positions (b's thread wrote the entry above)
+    if (refused) a.cu_q[b + 1] = 0;
+  }
   if (threadIdx.x == 0) {
     a.cu_q[0] = 0;
     a.head->refused = refused;

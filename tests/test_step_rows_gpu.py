@@ -6,6 +6,7 @@ import torch
 
 from sparse_attention_long_dsa_b200 import binding as B
 from sparse_attention_long_dsa_b200 import workloads as W
+from sparse_attention_long_dsa_b200.paged_cache import PagedCache
 from sparse_attention_long_dsa_b200.pipeline import DeviceBatch
 
 pytestmark = pytest.mark.gpu
@@ -110,3 +111,28 @@ def test_a_decode_row_of_a_sequence_without_tokens(kind):
     assert (some.out[1::2] == 0).all() and torch.equal(some.out[::2], full.out[::2])
     assert (some.block_select(3)[1::2] == -1).all()
     some.check_status()
+
+
+# ------------------------------------------------------------------------------------------------ refused steps
+@pytest.mark.parametrize("rows", [600, 5000])                # plan and rows in one launch, and in two
+def test_a_refused_step_has_no_rows(rows):
+    """A prompt that does not fit: cu_q is zero, so that the calls which follow in a captured step find rows of no sequence
+    (the cached lengths with the prompt's rows would put them at negative positions)."""
+    cache = PagedCache(3, 12, 40)
+    cache.extend(_i32([100, 0, 70]), 170)
+    cache.check_status()
+    cache.extend(_i32([1, 2000, 1]), rows)
+    with pytest.raises(B.DSAError) as e:
+        cache.check_status()
+    assert e.value.status == B.DSA_ERR_DEVICE_CHECK
+    assert cache.cu_q.tolist() == [0] * 4 and cache.seq_lens.tolist() == [100, 0, 70]
+    assert (cache.slots == -1).all() and (cache.positions == -1).all()
+    batch = B.make_batch(cache.block_table, cache.seq_lens, cache.cu_q, num_blocks=12, page_size=64, total_q=rows,
+                         max_q_per_seq=2000, max_seq_len=2560)
+    ws = torch.zeros(B.dsa_workspace_size(B.DSA_OP_INDEXER_TOPK, batch, 64), dtype=torch.uint8, device=DEV)
+    q, w = torch.zeros((rows, 64, 128), dtype=torch.uint8, device=DEV), torch.ones((rows, 64), device=DEV)
+    scores, idx = torch.full((rows, 2560), -77.0, device=DEV), torch.zeros((rows, 64), dtype=torch.int32, device=DEV)
+    B.dsa_indexer_topk(q, B.DSA_FP8_E4M3, w, cache.ki_pool, B.DSA_FP8_E4M3, cache.ks_pool, 64, 128, batch, 64, scores, 2560,
+                       idx, ws, ws.numel())
+    B.dsa_read_device_status(ws)
+    assert (scores == -77).all() and (idx == -1).all()
