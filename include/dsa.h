@@ -343,6 +343,9 @@ DSA_API dsa_status_t dsa_cp_merge(const void *part_out, dsa_dtype_t dt, const fl
  *   positions[r] = the position of query row r;  slots[r] = page_size * its block + position % page_size
  *   *free_left  = free blocks left
  *   Rows r in [cu_q[num_seqs], total_q) (total_q: capacity of slots and positions) get slot and position -1.
+ *   cu_q == NULL: a decode step laid out one row per sequence, as the decode calls take it, instead of packed rows: new_lens[b]
+ *       is 0 or 1 (else the step is refused), total_q == num_seqs, and row b is sequence b's new token, or has slot and
+ *       position -1 where there is none.
  *   seq_lens may be cached_lens itself and free_left may be free_count; no other arguments may overlap.
  *   A step that does not fit (a negative length, a sequence longer than its table row, more rows than total_q,
  *   fewer free blocks than needed, a count outside [0, free_capacity]) is refused as a whole: the table and the

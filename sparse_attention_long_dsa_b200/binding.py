@@ -321,20 +321,22 @@ def dsa_batch_extend(cached_lens, new_lens, page_size: int, num_blocks: int, tot
                      block_table, seq_lens, cu_q, slots, positions, free_left, ws, ws_bytes: int, stream=None):
     """Block tables, slots and positions of a step, from device lengths (cached_lens, new_lens [B]): block_table [B,
     max_blocks] and the stack free_blocks / free_count lose and gain pages on the device.  seq_lens may be cached_lens
-    and free_left may be free_count."""
+    and free_left may be free_count.  cu_q None: a decode step of one row per sequence (total_q = B, new_lens of 0 or 1)."""
     import torch
     w = "dsa_batch_extend"
     n, table_shape = cached_lens.numel(), block_table.shape
-    if new_lens.shape != (n,) or seq_lens.shape != (n,) or cu_q.shape != (n + 1,):
+    if new_lens.shape != (n,) or seq_lens.shape != (n,) or (cu_q is not None and cu_q.shape != (n + 1,)):
         raise DSAError(DSA_ERR_INVALID_ARG, w, f"new_lens {tuple(new_lens.shape)}, seq_lens {tuple(seq_lens.shape)}, cu_q "
-                       f"{tuple(cu_q.shape)}; expected ({n},), ({n},), ({n + 1},)")
+                       f"{None if cu_q is None else tuple(cu_q.shape)}; expected ({n},), ({n},), ({n + 1},)")
     if len(table_shape) != 2 or table_shape[0] != n or slots.numel() < total_q or positions.numel() < total_q:
         raise DSAError(DSA_ERR_INVALID_ARG, w, f"block_table [{n}, max_blocks], slots and positions [total_q] expected")
-    cached, new, free, count, table, seq, cu, pos, left = _dense(w, torch.int32, cached_lens, new_lens, free_blocks, free_count,
-                                                                 block_table, seq_lens, cu_q, positions, free_left)
+    cached, new, free, count, table, seq, pos, left, *cu = _dense(w, torch.int32, cached_lens, new_lens, free_blocks, free_count,
+                                                                  block_table, seq_lens, positions, free_left,
+                                                                  *(() if cu_q is None else (cu_q,)))
     slot, = _dense(w, torch.int64, slots)
     _check((_lib or load()).dsa_batch_extend(cached, new, n, page_size, table_shape[1], num_blocks, total_q, free,
-                                             free_blocks.numel(), count, table, seq, cu, slot, pos, left, _ptr(ws), ws_bytes,
+                                             free_blocks.numel(), count, table, seq, cu[0] if cu else None, slot, pos, left,
+                                             _ptr(ws), ws_bytes,
                                              _stream(stream, cached_lens.get_device())), w)
 
 

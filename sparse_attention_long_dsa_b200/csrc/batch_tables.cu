@@ -6,6 +6,7 @@
 //   block_table[b, held_b + i] = free_blocks[free_count - 1 - (sum_{a<b} need_a + i)],   0 <= i < need_b
 //   seq_lens[b] = cached_b + new_b,   cu_q[b] = sum_{a<b} new_a
 //   slots[r] = 64 block_table[b, pos / 64] + pos % 64,   pos = positions[r] = cached_b + r - cu_q[b]
+// or, without cu_q, for new_b of 0 or 1, one row per sequence: positions[b] = cached_b, and slot and position -1 where new_b = 0.
 // ("Day-0 Adaptation: Running Trillion-Parameter Models on Domestic AI Accelerators", 3.2: paged cache, block table from
 // logical to physical blocks.)  Release is the inverse: the blocks of finished sequences go back on the stack.
 //
@@ -34,7 +35,7 @@ struct BtHead {
 
 struct ExtendArgs {
   const int32_t *cached, *add, *free_blocks, *free_count;
-  int32_t *table, *seq_lens, *cu_q, *positions, *free_left;
+  int32_t *table, *seq_lens, *cu_q, *positions, *free_left;      // cu_q nullptr: one row per sequence
   int64_t *slots;
   int num_seqs, max_blocks, num_blocks, total_q, free_cap;
   BtHead *head;                            // workspace
@@ -95,7 +96,7 @@ __device__ __forceinline__ void extend_plan(const ExtendArgs &a) {
     int32_t cached = 0;
     if (b < a.num_seqs) {
       const int64_t c = a.cached[b], n = a.add[b];
-      bad |= c < 0 || n < 0 || c + n > cap;
+      bad |= c < 0 || n < 0 || c + n > cap || (!a.cu_q && n > 1);
       cached = clamp31(c, cap);
       add = n < 0 ? 0 : n;
       const int32_t seq = clamp31(cached + add, cap);
@@ -106,7 +107,7 @@ __device__ __forceinline__ void extend_plan(const ExtendArgs &a) {
     if (b < a.num_seqs) {
       a.ws_cached[b] = cached;
       a.ws_first[b] = clamp31(need + en, 0x7FFFFFFF);
-      a.cu_q[b + 1] = clamp31(rows + er + add, a.total_q);
+      if (a.cu_q) a.cu_q[b + 1] = clamp31(rows + er + add, a.total_q);
     }
     rows += tr;
     need += tn;
@@ -117,10 +118,10 @@ __device__ __forceinline__ void extend_plan(const ExtendArgs &a) {
   for (int b = threadIdx.x; b < a.num_seqs; b += blockDim.x) {
     a.seq_lens[b] = a.ws_cached[b] + (refused ? 0 : a.add[b]);
     // no rows: cached lengths with the refused rows would put rows at negative positions (b's thread wrote the entry above)
-    if (refused) a.cu_q[b + 1] = 0;
+    if (refused && a.cu_q) a.cu_q[b + 1] = 0;
   }
   if (threadIdx.x == 0) {
-    a.cu_q[0] = 0;
+    if (a.cu_q) a.cu_q[0] = 0;
     a.head->refused = refused;
     a.head->rows = clamp31(rows, a.total_q);
     a.head->top = count;
@@ -129,10 +130,36 @@ __device__ __forceinline__ void extend_plan(const ExtendArgs &a) {
   }
 }
 
+// slot of token pos of sequence b (c tokens cached, the step's first new page `first` from the top of the stack), -1 for a bad
+// block id; the first row of a new page writes its table entry
+__device__ __forceinline__ int64_t place_token(const ExtendArgs &a, int b, int pos, int c, int first, int top) {
+  const int page = pos / kBtPage, held = (c + kBtPage - 1) / kBtPage;
+  int32_t *entry = a.table + (int64_t)b * a.max_blocks + page;
+  int32_t blk = page < held ? *entry : __ldg(a.free_blocks + (top - 1 - (first + page - held)));
+  int64_t slot = -1;
+  if ((unsigned)blk >= (unsigned)a.num_blocks) {
+    set_status(a.status, kStatusBadIndex);
+    blk = -1;
+  } else {
+    slot = (int64_t)blk * kBtPage + pos % kBtPage;
+  }
+  if (page >= held && pos % kBtPage == 0) *entry = blk;
+  return slot;
+}
+
 __device__ __forceinline__ void extend_rows(const ExtendArgs &a, int r0) {
   // the plan's results: written by this grid's own block or by the launch before, so not through the read-only path
   const int refused = a.head->refused, rows = a.head->rows, top = a.head->top;
   if (r0 >= a.total_q) return;
+  if (!a.cu_q) {                           // row b is sequence b; total_q == num_seqs
+    for (int b = r0; b < min(r0 + kBtRows, a.total_q); ++b) {
+      const bool has = !refused && a.add[b] > 0;
+      const int pos = has ? a.ws_cached[b] : -1;
+      a.positions[b] = pos;
+      a.slots[b] = has ? place_token(a, b, pos, pos, a.ws_first[b], top) : -1;
+    }
+    return;
+  }
   int b = 0;
   if (!refused && r0 < rows) {             // largest b with cu_q[b] <= r0
     int hi = a.num_seqs - 1;
@@ -158,16 +185,7 @@ __device__ __forceinline__ void extend_rows(const ExtendArgs &a, int r0) {
         first = a.ws_first[b];
       }
       pos = c + (r - q0);
-      const int page = pos / kBtPage, held = (c + kBtPage - 1) / kBtPage;
-      int32_t *entry = a.table + (int64_t)b * a.max_blocks + page;
-      int32_t blk = page < held ? *entry : __ldg(a.free_blocks + (top - 1 - (first + page - held)));
-      if ((unsigned)blk >= (unsigned)a.num_blocks) {
-        set_status(a.status, kStatusBadIndex);
-        blk = -1;
-      } else {
-        slot = (int64_t)blk * kBtPage + pos % kBtPage;
-      }
-      if (page >= held && pos % kBtPage == 0) *entry = blk;
+      slot = place_token(a, b, pos, c, first, top);
     }
     a.positions[r] = pos;
     a.slots[r] = slot;

@@ -578,8 +578,10 @@ dsa_status_t dsa_batch_extend(const int32_t *cached_lens, const int32_t *new_len
   if (st != DSA_OK) return st;
   CHECK_ARG(total_q >= 0, "total_q must be >= 0");
   CHECK_SUP(total_q <= 1 << 30, "total_q must be at most 2^30 (got %d)", total_q);
-  CHECK_ARG(cached_lens && new_lens && free_count && free_left && block_table && seq_lens && cu_q,
-            "cached_lens, new_lens, free_count, free_left, block_table, seq_lens and cu_q are required");
+  CHECK_ARG(cached_lens && new_lens && free_count && free_left && block_table && seq_lens,
+            "cached_lens, new_lens, free_count, free_left, block_table and seq_lens are required");
+  CHECK_ARG(cu_q || total_q == num_seqs, "without cu_q a step has one row per sequence: total_q (%d) must be num_seqs (%d)",
+            total_q, num_seqs);
   CHECK_ARG(free_capacity == 0 || free_blocks, "free_blocks is required");
   CHECK_ARG(total_q == 0 || (slots && positions), "slots and positions are required");
   CHECK_ARG(new_lens != seq_lens && new_lens != cached_lens, "new_lens may not be cached_lens or seq_lens");

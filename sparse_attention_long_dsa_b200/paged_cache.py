@@ -3,12 +3,17 @@
 `PagedCache` holds the three pools of the MLA path (latent rows, FP8 indexer keys, key scales) with the state that
 places tokens in them, and enqueues a serving step on one stream:
 
-    cache.extend(new_lens, total_q)            tables, slots, positions and cu_q of the step (dsa_batch_extend)
+    cache.extend(new_lens)                     a decode step, one row per sequence slot: tables, slots, positions
+    cache.extend(new_lens, total_q)            any step, rows packed by cu_q (dsa_batch_extend)
     cache.store(kv, k_idx, ...)                norms and rotation of the step's rows, written to their slots, and of
                                                its queries (dsa_qk_norm_rope)
     cache.attend(q, out, ...)                  one-token attention over every cached page or a list of pages
                                                (dsa_paged_attn_decode); or the sparse path on `cache.batch(...)`
     cache.release(done)                        finished sequences give their blocks back (dsa_batch_release)
+
+In a decode step row b of every tensor is slot b, paused and empty slots included, which is what `attend` and the decode calls
+take.  In a packed step rows follow one another by cu_q, so a slot without a new token shifts the rows behind it: its tensors
+go with `batch`, and `attend` then wants a q of its own, one row per slot.
 
 Nothing here computes any part of the method, and no call reads the device: a step that does not fit is refused on the
 device and shows in `check_status`.  Every call may be captured into a graph after its first run outside one.
@@ -44,23 +49,27 @@ class PagedCache:
         self.free_count = torch.full((1,), num_blocks, dtype=torch.int32, device=dv)
         self._rows = {}                              # rows -> (slots, positions): kept, so that captured steps stay valid
         self.slots = self.positions = None
+        self.packed = True                           # how the last step's rows are laid out
         self._one_each = torch.arange(num_seqs + 1, dtype=torch.int32, device=dv)
         size = max(B.dsa_batch_workspace_size(B.DSA_OP_BATCH_EXTEND, num_seqs),
                    B.dsa_workspace_size(B.DSA_OP_PAGED_DECODE, self.decode_batch(), 0, heads, VALUE))
         self.ws = torch.zeros(size, dtype=torch.uint8, device=dv)
 
-    def extend(self, new_lens, total_q: int, stream=None):
-        """A step of new_lens [num_seqs] tokens (device int32), total_q of them or fewer: grows the tables and lengths and
-        fills cu_q, slots [total_q] and positions [total_q].  Steps of similar sizes write the same buffers."""
-        cap = 1 << max(0, total_q - 1).bit_length()
+    def extend(self, new_lens, total_q=None, stream=None):
+        """A step of new_lens [num_seqs] tokens (device int32): grows the tables and lengths and fills slots and positions.
+        total_q None: a decode step, new_lens of 0 or 1, one row per slot (slot and position -1 where it is 0); cu_q stays as
+        it was.  Otherwise rows are packed, total_q of them or fewer, and cu_q is filled; rows behind the last one have slot
+        and position -1.  Steps of similar sizes write the same buffers."""
+        rows = self.num_seqs if total_q is None else total_q
+        cap = 1 << max(0, rows - 1).bit_length()
         if cap not in self._rows:
             self._rows[cap] = (torch.empty(cap, dtype=torch.int64, device=self.device),
                                torch.empty(cap, dtype=torch.int32, device=self.device))
         slots, positions = self._rows[cap]
-        self.slots, self.positions = slots[:total_q], positions[:total_q]
-        B.dsa_batch_extend(self.seq_lens, new_lens, PAGE, self.num_blocks, total_q, self.free_blocks, self.free_count,
-                           self.block_table, self.seq_lens, self.cu_q, self.slots, self.positions, self.free_count, self.ws,
-                           self.ws.numel(), stream)
+        self.slots, self.positions, self.packed = slots[:rows], positions[:rows], total_q is not None
+        B.dsa_batch_extend(self.seq_lens, new_lens, PAGE, self.num_blocks, rows, self.free_blocks, self.free_count,
+                           self.block_table, self.seq_lens, self.cu_q if self.packed else None, self.slots, self.positions,
+                           self.free_count, self.ws, self.ws.numel(), stream)
 
     def release(self, done, stream=None):
         """Sequences with done[b] != 0 give their blocks back and become empty."""
@@ -68,11 +77,16 @@ class PagedCache:
                             self.ws, self.ws.numel(), stream)
 
     def store(self, kv, kv_weight, inv_freq, k_idx=None, k_idx_weight=None, q_rot=None, q=None, q_idx=None, q_idx_out=None,
-              eps: float = 1e-6, stream=None):
-        """The step's rows, total_q of them: kv [total_q, 576] (512 normed by kv_weight, 64 rotated in pairs) and k_idx
-        [total_q, 128] (normed by k_idx_weight, its first 64 rotated in halves, e4m3 with a scale) go to their slots; q_rot
-        [total_q, heads, 64] is rotated into q[:, :, 512:] and q_idx [total_q, 64, 128] (first 64 rotated in halves) into
-        q_idx_out as e4m3 codes.  Up to three of them may be left out."""
+              eps: float = 1e-6, stream=None, packed: bool = False):
+        """The step's rows, total_q of them (a decode step: num_seqs): kv [total_q, 576] (512 normed by kv_weight, 64 rotated in
+        pairs) and k_idx [total_q, 128] (normed by k_idx_weight, its first 64 rotated in halves, e4m3 with a scale) go to their
+        slots; q_rot [total_q, heads, 64] is rotated into q[:, :, 512:] and q_idx [total_q, 64, 128] (first 64 rotated in halves)
+        into q_idx_out as e4m3 codes, row by row.  Up to three of them may be left out.  A packed step of num_seqs rows makes
+        a q that attend would take with its rows shifted behind a slot without a new token: it is refused unless packed says
+        that the packed rows are meant."""
+        if q_rot is not None and self.packed and not packed and self.num_seqs > 1 and q_rot.shape[0] == self.num_seqs:
+            raise B.DSAError(B.DSA_ERR_INVALID_ARG, "store", "queries of a packed step of num_seqs rows: extend without total_q lays "
+                             "a decode step out one row per slot, as attend takes it; packed=True keeps the packed rows")
         parts = [B.rope_part(kv, self.kv_pool.view(-1, LATENT), weight=kv_weight, norm=(0, VALUE), eps=eps, rope=(VALUE, ROPE),
                              slots=self.slots)]
         if k_idx is not None:
@@ -85,18 +99,27 @@ class PagedCache:
         B.dsa_qk_norm_rope(parts, self.positions, inv_freq, self.ws, self.ws.numel(), stream)
 
     def batch(self, total_q: int, max_q_per_seq: int, max_seq_len: int):
-        """The step's batch descriptor for the other calls (upper bounds as in make_batch)."""
-        return B.make_batch(self.block_table, self.seq_lens, self.cu_q, num_blocks=self.num_blocks, page_size=PAGE,
-                            total_q=total_q, max_q_per_seq=max_q_per_seq, max_seq_len=max_seq_len)
+        """The last step's batch descriptor for the other calls: total_q as in extend (num_seqs for a decode step), upper bounds of
+        rows per sequence and of lengths.  A packed step's is never a decode batch (its rows need not be the slots'), so the
+        sparse attention on it is dsa_sparse_attn_prefill."""
+        if not self.packed:
+            if total_q != self.num_seqs:
+                raise B.DSAError(B.DSA_ERR_INVALID_ARG, "batch", f"total_q {total_q}; a decode step has {self.num_seqs} rows")
+            return self._batch(self._one_each, total_q, 1, max_seq_len)
+        most = max(2, max_q_per_seq, -(-total_q // self.num_seqs))
+        return self._batch(self.cu_q, total_q, most, max(max_seq_len, most))
+
+    def _batch(self, cu_q, total_q, max_q_per_seq, max_seq_len):
+        return B.make_batch(self.block_table, self.seq_lens, cu_q, num_blocks=self.num_blocks, page_size=PAGE, total_q=total_q,
+                            max_q_per_seq=max_q_per_seq, max_seq_len=max_seq_len)
 
     def decode_batch(self):
         """One row per sequence slot, empty ones included."""
-        return B.make_batch(self.block_table, self.seq_lens, self._one_each, num_blocks=self.num_blocks, page_size=PAGE,
-                            total_q=self.num_seqs, max_q_per_seq=1, max_seq_len=self.max_blocks * PAGE)
+        return self._batch(self._one_each, self.num_seqs, 1, self.max_blocks * PAGE)
 
     def attend(self, q, out, softmax_scale: float, pages=None, lse=None, stream=None):
-        """q [num_seqs, heads, 576] over every cached token of its sequence, or over the tokens of the pages in pages
-        [num_seqs, kb] (int32, -1: none); out [num_seqs, heads, 512].  Empty slots give zeros."""
+        """q [num_seqs, heads, 576], row b of slot b, over every cached token of its sequence, or over the tokens of the pages in
+        pages [num_seqs, kb] (int32, -1: none); out [num_seqs, heads, 512].  Empty slots give zeros."""
         B._shape(q, (self.num_seqs, self.heads, LATENT), "attend")
         B._shape(out, (self.num_seqs, self.heads, VALUE), "attend")
         B._dense("attend", torch.bfloat16, q, out)

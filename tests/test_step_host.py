@@ -62,6 +62,11 @@ def test_extend_refusals(bad, status):
     assert _extend(**bad) == status
 
 
+@pytest.mark.parametrize("rows", [3, 5, 0])
+def test_without_cu_q_a_step_has_one_row_per_sequence(rows):
+    assert _extend(cu=None, rows=rows) == B.DSA_ERR_INVALID_ARG and "one row per sequence" in _err()
+
+
 @pytest.mark.parametrize("bad,status", [
     (dict(n=0), B.DSA_ERR_INVALID_ARG),
     (dict(page=32), B.DSA_ERR_UNSUPPORTED),

@@ -8,6 +8,7 @@ from sparse_attention_long_dsa_b200 import binding as B
 from sparse_attention_long_dsa_b200 import workloads as W
 from sparse_attention_long_dsa_b200.paged_cache import PagedCache
 from sparse_attention_long_dsa_b200.pipeline import DeviceBatch
+from test_step_gpu import _check, _extend_ref, _freq, _random_tables, _rope_ref, _Tables, _view
 
 pytestmark = pytest.mark.gpu
 
@@ -136,3 +137,196 @@ def test_a_refused_step_has_no_rows(rows):
                        idx, ws, ws.numel())
     B.dsa_read_device_status(ws)
     assert (scores == -77).all() and (idx == -1).all()
+
+
+# ------------------------------------------------------------------------------------------------ one row per sequence slot
+@pytest.mark.parametrize("cached,add", [
+    ([0], [1]),
+    ([63, 64, 65, 0, 127, 128], [1, 0, 1, 1, 1, 0]),
+    ([5, 64, 64], [0, 0, 0]),
+    ([64 * (i % 3) for i in range(3000)], [i % 2 for i in range(3000)]),              # plan and rows in two launches
+])
+def test_a_decode_step_has_one_row_per_sequence(cached, add):
+    n, rng = len(cached), np.random.default_rng(len(cached))
+    width, blocks, table, free = _random_tables(rng, cached, add, spare=3)
+    t = _Tables(n, width, blocks, free, table)
+    seq, slots = torch.full((n,), -5, dtype=torch.int32, device=DEV), torch.full((n,), -5, dtype=torch.int64, device=DEV)
+    pos, left = torch.full((n,), -5, dtype=torch.int32, device=DEV), torch.full((1,), -5, dtype=torch.int32, device=DEV)
+    B.dsa_batch_extend(_i32(cached), _i32(add), 64, blocks, n, t.free, t.count, t.table, seq, None, slots, pos, left, t.ws,
+                       t.ws.numel())
+    ref_table, ref_left, cu, ref_slots, ref_pos = _extend_ref(cached, add, table, free, sum(add))
+    assert t.status() == B.DSA_OK
+    assert np.array_equal(t.table.cpu(), ref_table) and left.item() == ref_left
+    assert np.array_equal(seq.cpu(), np.add(cached, add))
+    has, row = np.array(add) > 0, np.array(cu[:-1])
+    want = np.full((2, n), -1)
+    want[:, has] = ref_slots[row[has]], ref_pos[row[has]]
+    assert np.array_equal(slots.cpu(), want[0]) and np.array_equal(pos.cpu(), want[1])
+
+
+@pytest.mark.parametrize("bad", ["two tokens", "blocks"])
+def test_a_decode_step_that_does_not_fit(bad):
+    cache = PagedCache(3, 3 if bad == "two tokens" else 2, 4, 4)
+    cache.extend(_i32([64, 0, 64]), 128)
+    cache.check_status()
+    table, lens, count = cache.block_table.clone(), cache.seq_lens.clone(), cache.free_count.item()
+    cache.extend(_i32([0, 0, 2] if bad == "two tokens" else [1, 1, 0]))
+    with pytest.raises(B.DSAError) as e:
+        cache.check_status()
+    assert e.value.status == B.DSA_ERR_DEVICE_CHECK
+    assert torch.equal(cache.block_table, table) and torch.equal(cache.seq_lens, lens) and cache.free_count.item() == count
+    assert cache.slots.tolist() == cache.positions.tolist() == [-1] * 3
+
+
+def _check_sparse(c, q, out, lse, idx, live):
+    """Every position selected: the sparse attention of the live rows against the dense definition; others select nothing."""
+    for b, n in enumerate(c.lens_h):
+        if b in live:
+            assert idx[b].tolist() == list(range(n)) + [-1] * (idx.shape[1] - n)
+    keep = c.lens_h
+    c.lens_h = [n if b in live else 0 for b, n in enumerate(keep)]
+    masked, lm = out.clone(), lse.clone()
+    dead = [b for b in range(len(keep)) if b not in live]
+    masked[dead], lm[dead] = 0, -float("inf")
+    c.check(q, 0.07, masked, lm)
+    c.lens_h = keep
+
+
+def test_a_captured_decode_step_with_pauses_from_store_to_both_attentions():
+    """Tables, stores, scores, selection, sparse and dense attention of a decode step in one graph, q and the indexer's queries
+    taken from store.  Slots pause in the middle and at the front; one stays empty.  Row b is slot b throughout."""
+    n, heads, k = 5, 128, 256
+    cache = PagedCache(n, 30, 4, heads)
+    rng = np.random.default_rng(21)
+    f = lambda *s: torch.tensor(rng.standard_normal(s), device=DEV).bfloat16()        # noqa: E731
+    w_kv, w_ki, freq = f(512).abs() + 0.5, f(128).abs() + 0.5, torch.tensor(_freq(64), device=DEV)
+    cache.extend(_i32([70, 100, 3, 62, 0]), 240)
+    cache.store(f(240, 576), w_kv, freq, k_idx=f(240, 128), k_idx_weight=w_ki)
+    new, kv, k_idx, q_rot, q_idx = _i32([0] * n), f(n, 576), f(n, 128), f(n, heads, 64), f(n, 64, 128)
+    q, q_idx_out = f(n, heads, 576), torch.zeros((n, 64, 128), dtype=torch.uint8, device=DEV)
+    w, scores = torch.rand((n, 64), device=DEV), torch.zeros((n, 256), device=DEV)
+    idx = torch.zeros((n, k), dtype=torch.int32, device=DEV)
+    outs = [torch.empty((n, heads, 512), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    lses = [torch.empty((n, heads), device=DEV) for _ in range(2)]
+    sparse = cache.decode_batch()
+    size = max(B.dsa_workspace_size(B.DSA_OP_INDEXER_TOPK, sparse, k), B.dsa_workspace_size(B.DSA_OP_ATTN_DECODE, sparse, k, heads, 512))
+    ws = torch.zeros(size, dtype=torch.uint8, device=DEV)
+
+    def step():
+        cache.extend(new)
+        cache.store(kv, w_kv, freq, k_idx=k_idx, k_idx_weight=w_ki, q_rot=q_rot, q=q, q_idx=q_idx, q_idx_out=q_idx_out)
+        batch = cache.batch(n, 1, 256)
+        B.dsa_indexer_topk(q_idx_out, B.DSA_FP8_E4M3, w, cache.ki_pool, B.DSA_FP8_E4M3, cache.ks_pool, 64, 128, batch, k, scores,
+                           256, idx, ws, size)
+        B.dsa_sparse_attn_decode(q, B.DSA_BF16, cache.kv_pool, None, heads, 576, 512, 0.07, idx, k, batch, outs[0], lses[0], ws, size)
+        cache.attend(q, outs[1], 0.07, lse=lses[1])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()                                                         # no slot has a new token
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    lens = np.array([70, 100, 3, 62, 0])
+    for add in ([1, 0, 1, 1, 0], [0, 1, 1, 1, 0], [1, 1, 0, 1, 0], [0, 0, 1, 0, 1], [1, 1, 1, 1, 1]):
+        new.copy_(_i32(add))
+        for x in (kv, k_idx, q_rot, q_idx, q):
+            x.copy_(f(*x.shape))
+        before = q.clone()
+        graph.replay()
+        lens += add
+        cache.check_status()
+        B.dsa_read_device_status(ws)
+        live = [b for b in range(n) if add[b]]
+        assert cache.seq_lens.tolist() == lens.tolist()
+        assert cache.positions.tolist() == [lens[b] - 1 if add[b] else -1 for b in range(n)]
+        ref, pre = _rope_ref(q_rot.double().cpu().numpy(), lens - 1, 1, (0, 0), 0, (0, 64), "pairs")
+        _check(q[live][:, :, 512:], ref[live], pre[live], "bf16")
+        rest = [b for b in range(n) if not add[b]]
+        assert torch.equal(q[rest], before[rest]) and torch.equal(q[:, :, :512], before[:, :, :512])
+        c = _view(cache, heads)
+        c.check(q, 0.07, outs[1], lses[1])
+        _check_sparse(c, q, outs[0], lses[0], idx, live)
+
+
+def test_a_captured_packed_step_with_padding_and_pauses():
+    """A packed step through batch: capacity above the rows, a slot without rows in the middle; scores, selection and sparse
+    attention row by row.  With as many rows as slots the descriptor is still no decode batch."""
+    n, heads, t, k = 3, 128, 7, 128
+    cache = PagedCache(n, 20, 3, heads)
+    rng = np.random.default_rng(22)
+    f = lambda *s: torch.tensor(rng.standard_normal(s), device=DEV).bfloat16()        # noqa: E731
+    w_kv, w_ki, freq = f(512).abs() + 0.5, f(128).abs() + 0.5, torch.tensor(_freq(64), device=DEV)
+    lens = np.array([60, 1, 64])
+    cache.extend(_i32(lens), 125)
+    cache.store(f(125, 576), w_kv, freq, k_idx=f(125, 128), k_idx_weight=w_ki)
+    for t, adds in ((7, ([2, 0, 3], [1, 1, 1], [0, 0, 0], [0, 0, 7])), (3, ([1, 0, 1], [0, 2, 1], [0, 1, 1]))):
+        new, kv, k_idx, q_rot, q_idx = _i32([0] * n), f(t, 576), f(t, 128), f(t, heads, 64), f(t, 64, 128)
+        q, q_idx_out = f(t, heads, 576), torch.zeros((t, 64, 128), dtype=torch.uint8, device=DEV)
+        w, scores = torch.rand((t, 64), device=DEV), torch.zeros((t, 192), device=DEV)
+        idx = torch.zeros((t, k), dtype=torch.int32, device=DEV)
+        out = torch.empty((t, heads, 512), dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty((t, heads), device=DEV)
+
+        def step():
+            cache.extend(new, t)
+            cache.store(kv, w_kv, freq, k_idx=k_idx, k_idx_weight=w_ki, q_rot=q_rot, q=q, q_idx=q_idx, q_idx_out=q_idx_out,
+                        packed=True)
+            batch = cache.batch(t, 1 if t == n else t, 192)
+            size = max(B.dsa_workspace_size(B.DSA_OP_INDEXER_TOPK, batch, k),
+                       B.dsa_workspace_size(B.DSA_OP_ATTN_PREFILL, batch, k, heads, 512))
+            B.dsa_indexer_topk(q_idx_out, B.DSA_FP8_E4M3, w, cache.ki_pool, B.DSA_FP8_E4M3, cache.ks_pool, 64, 128, batch, k,
+                               scores, 192, idx, ws, size)
+            B.dsa_sparse_attn_prefill(q, B.DSA_BF16, cache.kv_pool, None, heads, 576, 512, 0.07, idx, k, batch, out, lse, ws, size)
+
+        ws = torch.zeros(1 << 26, dtype=torch.uint8, device=DEV)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for add in adds:
+            new.copy_(_i32(add))
+            graph.replay()
+            lens = lens + add
+            cache.check_status()
+            B.dsa_read_device_status(ws)
+            assert cache.seq_lens.tolist() == lens.tolist()
+            c = _view(cache, heads)
+            seq = np.repeat(np.arange(n), add)
+            rows = [lens[b] - add[b] + i + 1 for b in range(n) for i in range(add[b])]
+            c.table_h = np.concatenate([c.table_h[seq], np.zeros((t - len(seq), 3), int)])
+            c.lens_h = rows + [0] * (t - len(rows))
+            for r, m in enumerate(c.lens_h):
+                m = min(m, k)
+                if c.lens_h[r] <= k:
+                    assert idx[r].tolist() == list(range(m)) + [-1] * (k - m)
+            assert max(c.lens_h) <= k
+            c.check(q, 0.07, out, lse)
+
+
+def test_queries_of_a_packed_step_of_num_seqs_rows():
+    """attend would take them with rows shifted behind a pause: refused, unless the caller says that packed rows are meant."""
+    cache = PagedCache(3, 6, 2, 4)
+    w, freq = torch.ones(512, device=DEV), torch.tensor(_freq(64), device=DEV)
+    kv, q_rot = torch.randn((3, 576), device=DEV).bfloat16(), torch.randn((3, 4, 64), device=DEV).bfloat16()
+    q = torch.zeros((3, 4, 576), dtype=torch.bfloat16, device=DEV)
+    cache.extend(_i32([1, 0, 1]), 3)
+    with pytest.raises(B.DSAError) as e:
+        cache.store(kv, w, freq, q_rot=q_rot, q=q)
+    assert e.value.status == B.DSA_ERR_INVALID_ARG
+    cache.store(kv, w, freq)
+    cache.store(kv, w, freq, q_rot=q_rot, q=q, packed=True)
+    assert (q[:2, :, 512:] != 0).any(-1).all() and (q[2] == 0).all()                 # rows 0 and 1 are slots 0 and 2
+    q.zero_()
+    cache.extend(_i32([1, 0, 1]))
+    cache.store(kv, w, freq, q_rot=q_rot, q=q)
+    assert (q[::2, :, 512:] != 0).any(-1).all() and (q[1] == 0).all()
+    with pytest.raises(B.DSAError):
+        cache.batch(2, 1, 64)
+    cache.check_status()
