@@ -392,7 +392,8 @@ DSA_API dsa_status_t dsa_batch_release(const int32_t *done, int32_t num_seqs, in
  *   (NULL only when no part rotates: every row is taken);  inv_freq [rope_len / 2] f64 radians per position, shared
  *   by the parts, whose non-zero rope_len must be equal;  slots [T] int64.
  * Supported: 1 to 4 parts; T <= 2^30; D a multiple of 8 in [8, 1024]; norm_off, norm_len and rope_off multiples of 8; rope_len a
- * multiple of 16 up to 256; out strides >= D.  The workspace only carries the status word (256 bytes). */
+ * multiple of 16 up to 256; out strides >= D, and no two (row, head) of out may overlap: a row's heads lie before the next row,
+ * or a head's rows before the next head.  The workspace only carries the status word (256 bytes). */
 typedef enum { DSA_ROPE_PAIRS = 0, DSA_ROPE_HALVES = 1 } dsa_rope_style_t;
 typedef struct {
   const void *x;

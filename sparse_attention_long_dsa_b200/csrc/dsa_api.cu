@@ -638,7 +638,11 @@ static dsa_status_t check_rope_part(const dsa_rope_part_t *p, int i, int32_t T, 
   }
   CHECK_ARG(p->out_scale == nullptr || p->out_dt == DSA_FP8_E4M3, "part %d: out_scale goes with e4m3 output", i);
   CHECK_ARG(p->x_row_stride >= 0 && p->x_head_stride >= 0, "part %d: negative strides", i);
-  CHECK_ARG(p->out_row_stride >= p->D && (p->H == 1 || p->out_head_stride >= p->D),
+  // no two (row, head) share an entry: the heads of a row lie before the next row, or the rows of a head before the next head
+  CHECK_ARG(p->out_row_stride >= p->D &&
+                (p->H == 1 || (p->out_head_stride >= p->D &&
+                               ((p->out_row_stride - p->D) / p->out_head_stride >= p->H - 1 ||
+                                (p->out_head_stride - p->D) / p->out_row_stride >= p->out_rows - 1))),
             "part %d: output rows and heads overlap", i);
   CHECK_ARG(p->slots ? p->out_rows >= 1 : p->out_rows >= T, "part %d: out_rows (%lld) is too small", i,
             (long long)p->out_rows);

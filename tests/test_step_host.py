@@ -139,6 +139,29 @@ def test_rope_call_refusals():
     assert _lib().dsa_qk_norm_rope(None, 1, P, 1, P, P, 256, None) == B.DSA_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("H,rows,row,head,ok", [
+    (2, 10, 64, 64, False),                            # row t's second head is row t + 1's first
+    (3, 10, 191, 64, False),
+    (3, 10, 192, 64, True),
+    (3, 10, 64, 639, False),                           # heads first
+    (3, 10, 64, 640, True),
+    (3, 10, 100, 963, False),
+    (3, 10, 100, 964, True),
+    (128, 10, 128 * 576, 576, True),                   # a view of 64 entries of wider rows
+    (128, 10, 127 * 576 + 63, 576, False),
+    (2, 1 << 40, 64, 1 << 46, True),                   # strides whose products pass 64 bits
+    (2, 1 << 60, 1 << 60, 1 << 60, False),
+    (2, 1 << 60, 1 << 60, 64, True),
+    (1, 10, 64, 0, True),
+])
+def test_rope_output_rows_and_heads_may_not_overlap(H, rows, row, head, ok):
+    part = _part(H=H, D=64, norm_len=0, rope_off=0, x_row_stride=64 * H, x_head_stride=64, out_rows=rows, out_row_stride=row,
+                 out_head_stride=head)
+    status = _rope([part], ws_bytes=128)               # the workspace is looked at after the parts
+    assert status == (B.DSA_ERR_WORKSPACE if ok else B.DSA_ERR_INVALID_ARG)
+    assert ok or "overlap" in _err()
+
+
 # ------------------------------------------------------------------------------------------------ paged attention
 def _batch(**kw):
     d = dict(num_seqs=3, page_size=64, num_blocks=40, max_blocks_per_seq=4, block_table=1 << 20, seq_lens=1 << 21,
