@@ -306,6 +306,20 @@ def _dense(what: str, dtype, *tensors):
     raise DSAError(DSA_ERR_INVALID_ARG, what, f"a tensor on another device than the current one, cuda:{torch.cuda.current_device()}")
 
 
+def _here(what: str, *tensors):
+    """_ptr of tensors that have to be on the current device: its kernels could not reach them anywhere else."""
+    at, cur = [], None
+    for t in tensors:
+        at.append(_ptr(t))
+        if t is not None and not isinstance(t, int):
+            if cur is None:
+                import torch
+                cur = torch._C._cuda_getDevice()
+            if t.get_device() != cur:
+                raise DSAError(DSA_ERR_INVALID_ARG, what, f"a tensor on cuda:{t.get_device()}; the current device is cuda:{cur}")
+    return at
+
+
 def _shape(t, shape: tuple, what: str):
     if t.shape != shape:
         raise DSAError(DSA_ERR_INVALID_ARG, what, f"shape {tuple(t.shape)}; expected {shape}")
@@ -336,7 +350,7 @@ def dsa_batch_extend(cached_lens, new_lens, page_size: int, num_blocks: int, tot
     slot, = _dense(w, torch.int64, slots)
     _check((_lib or load()).dsa_batch_extend(cached, new, n, page_size, table_shape[1], num_blocks, total_q, free,
                                              free_blocks.numel(), count, table, seq, cu[0] if cu else None, slot, pos, left,
-                                             _ptr(ws), ws_bytes,
+                                             *_here(w, ws), ws_bytes,
                                              _stream(stream, cached_lens.get_device())), w)
 
 
@@ -351,7 +365,7 @@ def dsa_batch_release(done, page_size: int, num_blocks: int, block_table, seq_le
         raise DSAError(DSA_ERR_INVALID_ARG, w, f"block_table [{n}, max_blocks] expected")
     d, table, seq, free, count = _dense(w, torch.int32, done, block_table, seq_lens, free_blocks, free_count)
     _check((_lib or load()).dsa_batch_release(d, n, page_size, block_table.shape[1], num_blocks, table, seq, free,
-                                              free_blocks.numel(), count, _ptr(ws), ws_bytes, _stream(stream)), w)
+                                              free_blocks.numel(), count, *_here(w, ws), ws_bytes, _stream(stream)), w)
 
 
 _PARTS = tuple(dsa_rope_part_t * n for n in range(5))
@@ -434,7 +448,8 @@ def dsa_qk_norm_rope(parts, positions, inv_freq, ws, ws_bytes: int, stream=None)
     pos = None if positions is None else _dense(w, torch.int32, positions)[0]
     freq = None if inv_freq is None else _dense(w, torch.float64, inv_freq)[0]
     arr = _PARTS[len(parts)](*parts)
-    _check((_lib or load()).dsa_qk_norm_rope(arr, len(parts), pos, T, freq, _ptr(ws), ws_bytes, _stream(stream, cur)), w)
+    _check((_lib or load()).dsa_qk_norm_rope(arr, len(parts), pos, T, freq, *_here(w, ws), ws_bytes,
+                                             _stream(stream, cur)), w)
 
 
 def page_list_width(pages, rows: int) -> int:
@@ -453,9 +468,10 @@ def page_list_width(pages, rows: int) -> int:
 def dsa_paged_attn_decode(q, dt: int, kv_pool, v_pool, H: int, Dqk: int, Dv: int, softmax_scale: float, pages, kb: int,
                           batch: dsa_batch_t, out, lse, ws, ws_bytes: int, stream=None):
     """Attention of one new token per sequence over every cached page, or over its list of pages [B, kb]."""
-    _check(load().dsa_paged_attn_decode(_ptr(q), dt, _ptr(kv_pool), _ptr(v_pool), H, Dqk, Dv, softmax_scale, _ptr(pages),
-                                        kb, ctypes.byref(batch), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
-                                        _stream(stream)), "dsa_paged_attn_decode")
+    w = "dsa_paged_attn_decode"
+    q, kv_pool, v_pool, pages, out, lse, ws = _here(w, q, kv_pool, v_pool, pages, out, lse, ws)
+    _check(load().dsa_paged_attn_decode(q, dt, kv_pool, v_pool, H, Dqk, Dv, softmax_scale, pages, kb, ctypes.byref(batch), out, lse,
+                                        ws, ws_bytes, _stream(stream)), w)
 
 
 def dsa_read_device_status(ws, stream=None):

@@ -221,3 +221,53 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(B.DSAError) as e:
         B.dsa_qk_norm_rope([], None, None, 1 << 24, 256)
     assert e.value.status == B.DSA_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------------------------------------ devices
+class _On:
+    """What the binding looks at of a dense device tensor, without the device."""
+    is_cuda = True
+
+    def __init__(self, device, at=P):
+        self.device_index, self.at = device, at
+
+    def get_device(self):
+        return self.device_index
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.at
+
+
+@pytest.mark.parametrize("where", [None, "q", "kv_pool", "pages", "out", "lse", "ws"])
+def test_paged_attention_takes_tensors_of_the_current_device(monkeypatch, where):
+    import torch
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    t = {n: _On(int(n == where)) for n in ("q", "kv_pool", "pages", "out", "lse", "ws")}
+    with pytest.raises(B.DSAError) as e:
+        B.dsa_paged_attn_decode(t["q"], B.DSA_BF16, t["kv_pool"], None, 128, 576, 512, 0.1, t["pages"], 4, _batch(), t["out"],
+                                t["lse"], t["ws"], 1024, stream=1)
+    # all here: the library is asked, and finds the workspace too small
+    assert e.value.status == (B.DSA_ERR_WORKSPACE if where is None else B.DSA_ERR_INVALID_ARG)
+    assert where is None or "cuda:1" in str(e.value)
+
+
+@pytest.mark.parametrize("call", ["extend", "release", "rotation"])
+@pytest.mark.parametrize("device", [0, 1])
+def test_workspaces_belong_to_the_current_device(monkeypatch, call, device):
+    import torch
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(B, "_dense", lambda what, dtype, *tensors: [P + 64 * i for i in range(len(tensors))])
+    i, table, ws = torch.zeros(4, dtype=torch.int32), torch.zeros((4, 2), dtype=torch.int32), _On(device)
+    with pytest.raises(B.DSAError) as e:
+        if call == "extend":
+            B.dsa_batch_extend(i, i, 64, 4, 4, i, i, table, i, torch.zeros(5, dtype=torch.int32), i, i, i, ws, 16, stream=1)
+        elif call == "release":
+            B.dsa_batch_release(i, 64, 4, table, i, i, i, ws, 16, stream=1)
+        else:
+            part = _part()
+            part.rows, part.device, part.rotated = 10, 0, 64
+            B.dsa_qk_norm_rope([part], torch.zeros(10, dtype=torch.int32), torch.zeros(32), ws, 16, stream=1)
+    assert e.value.status == (B.DSA_ERR_WORKSPACE if device == 0 else B.DSA_ERR_INVALID_ARG)
