@@ -105,9 +105,10 @@ __global__ void __launch_bounds__(32 * NW) paged_simt_kernel(const PsArgs a) {
   }
   pdl_wait();
   pdl_trigger();
-  // One row of 8 pages: 7.3 us with a page per worker, 9.0 with two.  More rows than workers, none of up to 8 pages cut: 220 rows of
-  // 1 - 3 pages, 13 heads of 32 17.8 us, 25.9 cut anywhere; 150 of 2 - 7 pages 15.1, 16.5; 160 of 5 pages 19.5, 17.8.
-  plan_pages(a.view, worker, gridDim.x, 1, 1, 8, S.tmp, &S.plan);
+  // One row of 8 pages: 7.3 us with a page per worker, 9.0 with two.  More rows than workers, whole against cut anywhere; the wider the
+  // rows, the more pages of waiting a cut is worth less than.  16 heads of 128: 220 rows of 3 pages 36.9 us, 40.6 cut, but 149 of 8 66.4,
+  // 47.6, and one of 8 beside 150 of one 34.3, 24.7; of 64: 26.7, 32.5; 39.1, 31.8; 20.9, 21.4; 13 of 32: 18.6, 26.4; 25.1, 24.3; 17.6, 19.7.
+  plan_pages(a.view, worker, gridDim.x, PagedRule{1, 1, 8, LT <= 16 ? 7 : 4, LT == 8 ? 7.f : LT == 16 ? 5.f : 2.f}, S.tmp, &S.plan);
   if (tid == 0) a.o.info[worker] = worker_info(a.view, S.plan);
 
   SegmentWalk walk(S.plan);

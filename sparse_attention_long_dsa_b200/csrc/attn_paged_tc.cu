@@ -45,14 +45,16 @@ constexpr int kPtD = 576, kPtDv = 512;
 constexpr int kPtHalf = kPage / 2;
 constexpr int kPtNBuf = 4;                         // page buffers, and score tiles
 constexpr int kPtRing = 8;                         // published pages in flight
-// Fewest pages of a worker, and the longest row that stays whole: a page takes 0.9 us of a pair, cutting a row 3 us.  One row of 4
+// Fewest pages of a worker, and the longest row that stays whole: a page takes 1.2 us of a pair, cutting a row 3 us.  One row of 4
 // pages 13.0 us whole, 14.3 in two pieces; 16 rows of 5 pages 14.6, 16.7; one row of 8 pages 14.5 us in pieces of two, 16.0 of
 // four; of 128 pages 20.4 in pieces of two, 19.2 of four (one row of 64 times min_slots takes twice as many).
 constexpr uint32_t kPtMinSlots = 2, kPtWhole = 5;
-// The longest row that stays whole when there are more rows than workers, for more heads than 32 and for up to 32 (the results and
-// q of a segment count less then).  128 heads: 128 rows of 8 pages 31.8 us, 40.4 cut anywhere; 100 rows of 8 - 13 pages 35.5, 40.8.  16 heads: 128 rows of
-// 2 - 7 pages 22.8, 25.9; 80 rows of 11 - 16 pages cut anywhere 30.4, 36.2 whole.
-constexpr uint32_t kPtUncutMany = 16, kPtUncutFew = 10;
+// More rows than workers, whole against cut anywhere.  128 heads: 128 rows of 8 pages 32.2 us, 40.5 cut, 100 of 8 - 13 37.8, 40.6; but
+// 75 of 16 (the longest worker has 32 pages, 16 more than the average) 44.4, 41.4, and one of 16 beside 74 of one 26.9, 18.5.
+// Up to 32 heads, where q and the results of a segment count less: 128 of 8 28.2, 30.8; 150 of 8 36.7, 33.4; 75 of 8 27.0, 24.0.
+__device__ __forceinline__ PagedRule pt_rule(int H) {
+  return H > 32 ? PagedRule{kPtMinSlots, kPtWhole, 16, 6, 12.f} : PagedRule{kPtMinSlots, kPtWhole, 10, 4, 5.f};
+}
 constexpr int kPtThreads = 384;                    // softmax x 8, keys, QK^T, P V, values
 constexpr int kPtGroup = 128;                      // threads of a softmax group (4 warps)
 constexpr int kPtWarpKeys = 8, kPtWarpQK = 9, kPtWarpPV = 10, kPtWarpValues = 11;
@@ -224,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
   // inputs come from earlier work on the stream
   pdl_wait();
   pdl_trigger();
-  plan_pages(a.view, pair, npairs, kPtMinSlots, kPtWhole, a.H > 32 ? kPtUncutMany : kPtUncutFew, S->tmp, &S->plan);
+  plan_pages(a.view, pair, npairs, pt_rule(a.H), S->tmp, &S->plan);
 
   // next entry of the ring, for a whole warp: false ends the role (the end of the work, or a wait that ran out)
   auto next_entry = [&](uint32_t &ec, int4 *e) -> bool {

@@ -36,6 +36,15 @@ struct PagedOut {
   uint32_t *status;
 };
 
+// How finely rows may be cut, in page slots.
+struct PagedRule {
+  uint32_t min_slots;           // a worker for every so many
+  uint32_t whole;               // rows up to this stay whole
+  uint32_t uncut;               // with more rows than workers, rows up to this too, unless a worker's range would get longer
+  uint32_t row_over;            //   than the average one by more than this through a single row
+  float range_over;             //   or than this through the number of rows, which the workers share unevenly
+};
+
 struct PagedPlan {
   uint32_t total;               // P
   uint32_t start, end;          // this worker's slots
@@ -100,6 +109,14 @@ struct PlanThreads {
   }
   __device__ __forceinline__ bool all(bool x) const { return kWarp ? __all_sync(0xffffffffu, x) : __syncthreads_and(x); }
   __device__ __forceinline__ bool any(bool x) const { return kWarp ? __any_sync(0xffffffffu, x) : __syncthreads_or(x); }
+  __device__ __forceinline__ int sum(uint32_t x) const {       // (a scan is four times the code)
+    if (threadIdx.x == 0) tmp[0] = 0;
+    __syncthreads();
+    x = __reduce_add_sync(0xffffffffu, x);
+    if ((threadIdx.x & 31) == 0) atomicAdd(tmp, x);
+    __syncthreads();
+    return (int)tmp[0];
+  }
   __device__ __forceinline__ int that(bool x) const { return kWarp ? __popc(__ballot_sync(0xffffffffu, x)) : __syncthreads_count(x); }
 };
 
@@ -135,11 +152,16 @@ __device__ __forceinline__ bool split_rows(const PlanThreads<kWarp> &th, int wor
 
 template <bool kWarp>
 __device__ __forceinline__ void make_plan(const PlanThreads<kWarp> &th, const PagedView &v, int worker, int workers,
-                                          uint32_t min_slots, uint32_t whole, uint32_t uncut, PagedPlan *p) {
+                                          const PagedRule &rule, PagedPlan *p) {
+  const uint32_t min_slots = rule.min_slots, whole = rule.whole;
   const int nt = th.count(), per = kWarp ? 1 : (v.T + nt - 1) / nt;
   const int r0 = min(v.T, (int)threadIdx.x * per), r1 = min(v.T, r0 + per);
-  uint32_t mine = 0;
-  for (int r = r0; r < r1; ++r) mine += (uint32_t)row_slots(v, r);
+  uint32_t mine = 0, some = 0;
+  for (int r = r0; r < r1; ++r) {
+    const uint32_t n = (uint32_t)row_slots(v, r);
+    mine += n;
+    some += n > 0;
+  }
   uint32_t total;
   const uint32_t before = th.scan(mine, &total);
   // A worker for every min_slots page slots, and rows of at most `whole` slots in one piece: cutting a row costs partial results
@@ -159,9 +181,15 @@ __device__ __forceinline__ void make_plan(const PlanThreads<kWarp> &th, const Pa
   if (v.T > 1) {
     const uint32_t n0 = total / (uint32_t)v.T;
     const bool same = th.all(mine == n0 * (uint32_t)(r1 - r0));
-    const int rows = same ? v.T : th.that(mine > 0);
-    if (rows > workers) keep = uncut;                  // no worker to spare for a piece of a row
-    const uint32_t limit = total / (uint32_t)np + kSegment;
+    const int rows = same ? v.T : per == 1 ? th.that(mine > 0) : th.sum(some);       // that hold tokens
+    // More rows than workers: a border that moves to a row's end saves a segment, partial results and their join, but the call waits
+    // for the worker with the most rows, ceil(rows / np) of them where the average one has rows / np.
+    const uint32_t mean = total / (uint32_t)np, limit = mean + kSegment;
+    if (rows > workers) {
+      // (approximate: divisions and branches here run cold, and cost a call up to 1 us)
+      const float each = __fdividef((float)rows, (float)np), idle = ceilf(each - 1e-3f) - each;
+      if (idle * (float)mean <= rule.range_over * each) keep = max(whole, min(rule.uncut, mean + rule.row_over));
+    }
     if (same && rows <= workers) {
       const uint32_t each = rows < np && n0 > whole ? (uint32_t)np / (uint32_t)rows : 1u;
       if (n0 / each <= limit) np = (int)each * rows;
@@ -221,10 +249,10 @@ __device__ __forceinline__ void make_plan(const PlanThreads<kWarp> &th, const Pa
 }
 
 // Every thread of the block calls this (blockDim.x a multiple of 32, at most 1024); `tmp` holds 33 words.
-__device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int workers, uint32_t min_slots, uint32_t whole,
-                                           uint32_t uncut, uint32_t *tmp, PagedPlan *p) {
-  if (v.T > 32) make_plan(PlanThreads<false>{tmp}, v, worker, workers, min_slots, whole, uncut, p);
-  else if (threadIdx.x < 32) make_plan(PlanThreads<true>{tmp}, v, worker, workers, min_slots, whole, uncut, p);
+__device__ __forceinline__ void plan_pages(const PagedView &v, int worker, int workers, const PagedRule &rule, uint32_t *tmp,
+                                           PagedPlan *p) {
+  if (v.T > 32) make_plan(PlanThreads<false>{tmp}, v, worker, workers, rule, p);
+  else if (threadIdx.x < 32) make_plan(PlanThreads<true>{tmp}, v, worker, workers, rule, p);
   __syncthreads();
 }
 

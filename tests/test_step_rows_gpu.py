@@ -8,7 +8,7 @@ from sparse_attention_long_dsa_b200 import binding as B
 from sparse_attention_long_dsa_b200 import workloads as W
 from sparse_attention_long_dsa_b200.paged_cache import PagedCache
 from sparse_attention_long_dsa_b200.pipeline import DeviceBatch
-from test_step_gpu import _check, _extend_ref, _freq, _random_tables, _rope_ref, _Tables, _view
+from test_step_gpu import _Cache, _check, _extend_ref, _freq, _random_tables, _rope_ref, _Tables, _view
 
 pytestmark = pytest.mark.gpu
 
@@ -330,3 +330,43 @@ def test_queries_of_a_packed_step_of_num_seqs_rows():
     with pytest.raises(B.DSAError):
         cache.batch(2, 1, 64)
     cache.check_status()
+
+
+# ------------------------------------------------------------------------------------------------ which rows are cut
+def _cut_rows(c, heads, dv):
+    """The rows that were split, from what the attention left for its join in the workspace: (row, first worker) per worker."""
+    workers = 74 if dv > 128 else 148
+    info = c.ws[256:256 + 8 * workers].view(torch.int32).view(workers, 2).cpu().numpy()
+    return set(info[info[:, 0] >= 0, 0].tolist())
+
+
+_HALF = [10] * 100 + [0] * 500                             # more slots than threads, rows in a sixth of them
+
+
+@pytest.mark.parametrize("heads,f32,pages,cut", [
+    (128, None, [1] * 74 + [16], {74}),                    # a worker would wait for the one long row
+    (128, None, [2] * 80 + [16], {80}),
+    (128, None, [1] * 200 + [16, 16], {200, 201}),
+    (128, None, [75] * 2 + [6] * 75, {0, 1}),
+    (128, None, [16] * 75, None),                          # one worker would have two rows, 16 pages more than the others
+    (128, None, [8] * 128, set()),
+    (128, None, [8 + i % 6 for i in range(100)], set()),
+    (128, None, _HALF, set()),
+    (16, None, [8] * 75, None),
+    (16, None, [8] * 128, set()),
+    (16, (128, 128), [8] * 149, None),
+    (16, (128, 128), [3] * 220, set()),
+    (16, (128, 128), [1] * 150 + [8], {150}),
+    (13, (32, 32), [1] * 150 + [8], set()),
+    (4, (64, 64), [8] * 300, None),
+    (4, (64, 64), [3] * 220 + [0] * 300, set()),
+])
+def test_rows_stay_whole_where_no_worker_waits_for_them(heads, f32, pages, cut):
+    """More rows than workers.  cut: the rows in pieces; None: some are."""
+    c = _Cache([max(0, 64 * p - 7 * (i % 9)) for i, p in enumerate(pages)], f32=f32, seed=len(pages))
+    q = c.q(heads)
+    out, lse = c.attend(q, 0.07)
+    B.dsa_read_device_status(c.ws)
+    got = _cut_rows(c, heads, c.dv)
+    assert got == cut if cut is not None else got
+    c.check(q, 0.07, out, lse)
