@@ -64,6 +64,7 @@ constexpr uint32_t kPtQSize = 9 * 8192;
 constexpr uint32_t kPtP = 4096;                    // half of P: [64 heads][32 tokens] bf16, 64-byte swizzle
 constexpr uint32_t kPtTmemO = 0, kPtTmemS = 256;
 constexpr float kPtRescale = 8.0f;
+constexpr long long kPtSettle = 2000000;           // SM cycles, about 1 ms
 constexpr int kPtFirst = 1, kPtLast = 2, kPtEmpty = 4, kPtEnd = 8, kPtQ = 16;     // kPtQ: q of an empty segment was loaded
 
 struct PtSmem {
@@ -676,6 +677,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPtThreads, 1)
   // ---- teardown: every role is done; MMAs drained; the peer done with our barriers, buffers and TMEM
   tc::fence_before_sync();
   __syncthreads();
+  if (*abort) {
+    // A wait ran out, so that copies of keys, values or q may be on their way that no role will wait for, some counted on the other
+    // CTA's barrier.  They land long before this ends; their shared memory stays this pair's until then.
+    for (const long long t0 = clock64(); clock64() - t0 < kPtSettle;) {
+    }
+  }
   tc::cluster_sync();
   if (warp == kPtWarpPV) {
     tc::fence_after_sync();
