@@ -310,13 +310,17 @@ def _here(what: str, *tensors):
     """_ptr of tensors that have to be on the current device: its kernels could not reach them anywhere else."""
     at, cur = [], None
     for t in tensors:
-        at.append(_ptr(t))
         if t is not None and not isinstance(t, int):
+            on = t.get_device()
+            if on < 0 or not t.is_contiguous():
+                _ptr(t)                              # names a host or strided tensor
             if cur is None:
                 import torch
                 cur = torch._C._cuda_getDevice()
-            if t.get_device() != cur:
-                raise DSAError(DSA_ERR_INVALID_ARG, what, f"a tensor on cuda:{t.get_device()}; the current device is cuda:{cur}")
+            if on != cur:
+                raise DSAError(DSA_ERR_INVALID_ARG, what, f"a tensor on cuda:{on}; the current device is cuda:{cur}")
+            t = t.data_ptr()
+        at.append(t)
     return at
 
 
