@@ -982,3 +982,40 @@ def test_device_batch_paged_attention(kind):
         for b in range(5):
             ref, ref_lse = oracle.sparse_attention_row(wl, b, idx[b])
             assert np.abs(out[b] - ref).max() <= tol and np.abs(lse[b] - ref_lse).max() <= (1e-3 if kind == "mla" else 1e-5)
+
+
+@pytest.mark.parametrize("xd", ["f32", "bf16"])
+@pytest.mark.parametrize("t,h,d,norm,rope,style,slots", [
+    (5, 3, 64, (0, 64), (0, 64), "halves", True),          # 4, 8 and 32 lanes per row of a head
+    (9, 64, 128, (0, 0), (64, 64), "pairs", False),
+    (2, 150, 256, (0, 256), (0, 128), "halves", True),     # more heads than a CTA holds at a time
+    (4, 2, 1024, (512, 512), (0, 256), "pairs", True),
+    (600, 7, 128, (0, 128), (0, 64), "halves", True),
+])
+def test_a_scale_for_every_head(xd, t, h, d, norm, rope, style, slots):
+    """e4m3 codes with a scale per row and head: scale[row, head], and codes of the head's own scale."""
+    rng = np.random.default_rng(t + h)
+    n = t + 5
+    x = torch.tensor(rng.standard_normal((t, h, d)) * 10.0 ** rng.uniform(-2, 2, (t, h, 1)), device=DEV).to(_DT[xd])
+    x[1, 0] = 0
+    w = torch.tensor(1 + 0.3 * rng.standard_normal(max(norm[1], 1)), device=DEV).float() if norm[1] else None
+    pos = _positions(rng, t)
+    to = rng.permutation(n)[:t] if slots else np.arange(t)
+    out = torch.full((n, h, d), 0x55, dtype=torch.uint8, device=DEV)
+    scale = torch.full((n, h), 3.0, device=DEV)
+    ws = _zeros_ws(256)
+    part = B.rope_part(x, out, weight=w, norm=norm, rope=rope, style=style, scale=scale,
+                       slots=torch.tensor(to, device=DEV) if slots else None)
+    B.dsa_qk_norm_rope([part], _i32(pos), torch.tensor(_freq(rope[1]), device=DEV), ws, 256)
+    B.dsa_read_device_status(ws)
+    ref, pre = _rope_ref(x.double().cpu().numpy(), pos, 1 if w is None else w.double().cpu().numpy(), norm, float(np.float32(1e-6)),
+                         rope, style)
+    s = np.abs(ref).max(-1) / 448
+    s[s == 0] = 1
+    got = scale.double().cpu().numpy()[to]
+    assert (np.abs(got - s) <= pre.max(-1) / 448 + 4 * U * s).all()
+    q = ref / s[..., None]
+    slack = pre / s[..., None] + np.abs(q) * (pre.max(-1) / (448 * s) + 4 * U)[..., None]
+    _check(out.view(_DT["e4m3"])[torch.tensor(to, device=DEV)], q, slack, "e4m3")
+    rest = np.setdiff1d(np.arange(n), to)
+    assert (out[rest] == 0x55).all() and (scale[rest] == 3).all()
