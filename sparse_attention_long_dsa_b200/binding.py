@@ -457,13 +457,14 @@ def dsa_qk_norm_rope(parts, positions, inv_freq, ws, ws_bytes: int, stream=None)
 
 
 def page_list_width(pages, rows: int) -> int:
-    """kb of a page list [rows, kb] int32 on the current device; 0 for None (every page)."""
+    """kb of a page list [rows, kb] int32 on the current device; 0 for None (every page).  kb = 0 is refused: an empty tensor
+    has no address, so the library would take it for None."""
     import torch
     if pages is None:
         return 0
     w = "dsa_paged_attn_decode"
-    if pages.dim() != 2:
-        raise DSAError(DSA_ERR_INVALID_ARG, w, f"pages of {pages.dim()} dimensions; expected [{rows}, kb]")
+    if pages.dim() != 2 or pages.shape[1] == 0:
+        raise DSAError(DSA_ERR_INVALID_ARG, w, f"pages {tuple(pages.shape)}; expected [{rows}, kb], kb >= 1")
     _shape(pages, (rows, pages.shape[1]), w)
     _dense(w, torch.int32, pages)
     return pages.shape[1]
@@ -473,6 +474,8 @@ def dsa_paged_attn_decode(q, dt: int, kv_pool, v_pool, H: int, Dqk: int, Dv: int
                           batch: dsa_batch_t, out, lse, ws, ws_bytes: int, stream=None):
     """Attention of one new token per sequence over every cached page, or over its list of pages [B, kb]."""
     w = "dsa_paged_attn_decode"
+    if pages is not None and not isinstance(pages, int) and page_list_width(pages, batch.total_q) != kb:
+        raise DSAError(DSA_ERR_INVALID_ARG, w, f"pages {tuple(pages.shape)} with kb {kb}")
     q, kv_pool, v_pool, pages, out, lse, ws = _here(w, q, kv_pool, v_pool, pages, out, lse, ws)
     _check(load().dsa_paged_attn_decode(q, dt, kv_pool, v_pool, H, Dqk, Dv, softmax_scale, pages, kb, ctypes.byref(batch), out, lse,
                                         ws, ws_bytes, _stream(stream)), w)

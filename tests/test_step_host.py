@@ -241,17 +241,28 @@ class _On:
         return self.at
 
 
+class _Pages(_On):
+    def __init__(self, shape, dtype, device=0):
+        super().__init__(device, 0 if 0 in shape else P)          # an empty tensor's address is NULL
+        self.shape, self.dtype = shape, dtype
+
+    def dim(self):
+        return len(self.shape)
+
+
 @pytest.mark.parametrize("where", [None, "q", "kv_pool", "pages", "out", "lse", "ws"])
 def test_paged_attention_takes_tensors_of_the_current_device(monkeypatch, where):
     import torch
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
-    t = {n: _On(int(n == where)) for n in ("q", "kv_pool", "pages", "out", "lse", "ws")}
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    t = {n: _On(int(n == where)) for n in ("q", "kv_pool", "out", "lse", "ws")}
+    t["pages"] = _Pages((3, 4), torch.int32, int(where == "pages"))
     with pytest.raises(B.DSAError) as e:
         B.dsa_paged_attn_decode(t["q"], B.DSA_BF16, t["kv_pool"], None, 128, 576, 512, 0.1, t["pages"], 4, _batch(), t["out"],
                                 t["lse"], t["ws"], 1024, stream=1)
     # all here: the library is asked, and finds the workspace too small
     assert e.value.status == (B.DSA_ERR_WORKSPACE if where is None else B.DSA_ERR_INVALID_ARG)
-    assert where is None or "cuda:1" in str(e.value)
+    assert where in (None, "pages") or "cuda:1" in str(e.value)
 
 
 @pytest.mark.parametrize("call", ["extend", "release", "rotation"])
@@ -271,3 +282,18 @@ def test_workspaces_belong_to_the_current_device(monkeypatch, call, device):
             part.rows, part.device, part.rotated = 10, 0, 64
             B.dsa_qk_norm_rope([part], torch.zeros(10, dtype=torch.int32), torch.zeros(32), ws, 16, stream=1)
     assert e.value.status == (B.DSA_ERR_WORKSPACE if device == 0 else B.DSA_ERR_INVALID_ARG)
+
+
+@pytest.mark.parametrize("shape,kb,dtype", [
+    ((3, 0), 0, "int32"),                                    # lists that hold nothing are no request for every page
+    ((3, 4), 5, "int32"), ((2, 4), 4, "int32"), ((12,), 4, "int32"), ((3, 4), 4, "int64"),
+])
+def test_paged_attention_takes_page_lists_of_its_rows(monkeypatch, shape, kb, dtype):
+    import torch
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    t = [_On(0) for _ in range(5)]
+    with pytest.raises(B.DSAError) as e:
+        B.dsa_paged_attn_decode(t[0], B.DSA_BF16, t[1], None, 128, 576, 512, 0.1, _Pages(shape, getattr(torch, dtype)), kb,
+                                _batch(), t[2], t[3], t[4], 1024, stream=1)
+    assert e.value.status == B.DSA_ERR_INVALID_ARG
