@@ -386,7 +386,7 @@ DSA_API dsa_status_t dsa_batch_release(const int32_t *done, int32_t num_seqs, in
  *       h * out_head_stride: y rounded once to out_dt (e4m3 saturates at +-448)
  *   out_scale != NULL (e4m3 only): out_scale[row * H + h] = max|y| / 448 (1 if that is 0), codes of y / scale --
  *       the form dsa_cache_append stores indexer keys in.
- * Angles are reduced in 64 bits, so far positions lose nothing.  out may be x itself (same strides, no slots).  A
+ * Angles are reduced in 64 bits, so far positions lose nothing.  out may be x itself (same type and strides, no slots).  A
  * slot >= out_rows is skipped and reported as DSA_ERR_DEVICE_CHECK; two rows with the same slot race.
  *   x_dt f32 or bf16;  out_dt f32, bf16 or e4m3;  weight [norm_len] of w_dt f32 or bf16;  positions [T] int32
  *   (NULL only when no part rotates: every row is taken);  inv_freq [rope_len / 2] f64 radians per position, shared

@@ -644,6 +644,9 @@ static dsa_status_t check_rope_part(const dsa_rope_part_t *p, int i, int32_t T, 
                                ((p->out_row_stride - p->D) / p->out_head_stride >= p->H - 1 ||
                                 (p->out_head_stride - p->D) / p->out_row_stride >= p->out_rows - 1))),
             "part %d: output rows and heads overlap", i);
+  CHECK_ARG(p->out != p->x || (p->out_dt == p->x_dt && !p->slots && (T == 1 || p->out_row_stride == p->x_row_stride) &&
+                               (p->H == 1 || p->out_head_stride == p->x_head_stride)),
+            "part %d: out may be x only with x's type and strides, and without slots", i);
   CHECK_ARG(p->slots ? p->out_rows >= 1 : p->out_rows >= T, "part %d: out_rows (%lld) is too small", i,
             (long long)p->out_rows);
   const uintptr_t xa = p->x_dt == DSA_F32 ? 3 : 1;

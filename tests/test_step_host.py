@@ -162,6 +162,22 @@ def test_rope_output_rows_and_heads_may_not_overlap(H, rows, row, head, ok):
     assert ok or "overlap" in _err()
 
 
+@pytest.mark.parametrize("T,change,ok", [
+    (10, dict(), True),
+    (10, dict(x_dt=B.DSA_F32), False),                 # rows of f32 under rows of bf16: other rows' inputs are overwritten
+    (1, dict(x_dt=B.DSA_F32), False),
+    (10, dict(out_row_stride=1152), False),
+    (1, dict(out_row_stride=1152), True),              # one row has no stride
+    (10, dict(H=2, x_row_stride=1152, out_row_stride=1152), True),
+    (10, dict(H=2, x_row_stride=1152, x_head_stride=0, out_row_stride=1152), False),
+    (10, dict(slots=8 * P), False),
+    (10, dict(out=4 * P, slots=8 * P), True),
+])
+def test_rope_in_place_needs_the_same_layout(T, change, ok):
+    part = _part(**{**dict(out=P), **change})
+    assert _rope([part], T=T, ws_bytes=128) == (B.DSA_ERR_WORKSPACE if ok else B.DSA_ERR_INVALID_ARG)
+
+
 # ------------------------------------------------------------------------------------------------ paged attention
 def _batch(**kw):
     d = dict(num_seqs=3, page_size=64, num_blocks=40, max_blocks_per_seq=4, block_table=1 << 20, seq_lens=1 << 21,
