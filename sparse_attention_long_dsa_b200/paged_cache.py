@@ -84,6 +84,11 @@ class PagedCache:
         into q_idx_out as e4m3 codes, row by row.  Up to three of them may be left out.  A packed step of num_seqs rows makes
         a q that attend would take with its rows shifted behind a slot without a new token: it is refused unless packed says
         that the packed rows are meant."""
+        for name, x, dest, what in (("q_rot", q_rot, q, "q"), ("q_idx", q_idx, q_idx_out, "q_idx_out")):
+            if x is not None and dest is None:
+                raise B.DSAError(B.DSA_ERR_INVALID_ARG, "store", f"{name} goes with {what}")
+        if self.slots is None:
+            raise B.DSAError(B.DSA_ERR_INVALID_ARG, "store", "no step: extend first")
         if q_rot is not None and self.packed and not packed and self.num_seqs > 1 and q_rot.shape[0] == self.num_seqs:
             raise B.DSAError(B.DSA_ERR_INVALID_ARG, "store", "queries of a packed step of num_seqs rows: extend without total_q lays "
                              "a decode step out one row per slot, as attend takes it; packed=True keeps the packed rows")

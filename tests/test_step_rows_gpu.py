@@ -370,3 +370,22 @@ def test_rows_stay_whole_where_no_worker_waits_for_them(heads, f32, pages, cut):
     got = _cut_rows(c, heads, c.dv)
     assert got == cut if cut is not None else got
     c.check(q, 0.07, out, lse)
+
+
+def test_store_refusals():
+    cache = PagedCache(2, 4, 2, 4)
+    w, freq = torch.ones(512, device=DEV), torch.tensor(_freq(64), device=DEV)
+    f = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device=DEV)                   # noqa: E731
+    codes = torch.zeros((2, 64, 128), dtype=torch.uint8, device=DEV)
+    with pytest.raises(B.DSAError) as e:
+        cache.store(f(2, 576), w, freq)                                # no step yet: there are no slots to write to
+    assert e.value.status == B.DSA_ERR_INVALID_ARG
+    cache.extend(_i32([1, 1]))
+    for bad in (dict(q_rot=f(2, 4, 64)), dict(q_idx=f(2, 64, 128)), dict(k_idx=f(2, 128)), dict(q_rot=f(2, 3, 64), q=f(2, 4, 576)), dict(q_rot=f(3, 4, 64), q=f(3, 4, 576))):
+        with pytest.raises(B.DSAError) as e:
+            cache.store(f(2, 576), w, freq, **bad)
+        assert e.value.status == B.DSA_ERR_INVALID_ARG
+    with pytest.raises(B.DSAError):
+        cache.store(f(3, 576), w, freq)
+    cache.store(f(2, 576), w, freq, q_rot=f(2, 4, 64), q=f(2, 4, 576), q_idx=f(2, 64, 128), q_idx_out=codes)
+    cache.check_status()
