@@ -13,8 +13,8 @@
 // warp's own shared memory.  Warps are joined at the end of a segment, in their order.  Tokens past the sequence are not
 // loaded: what the cache holds there may be anything.
 // Bound by the issue of loads, FMAs and shuffles from two or three warps per scheduler (q, output, keys and values of a batch take most
-// of the registers).  16 rows of 256 - 8,192 tokens (61,000 in all, 31 MB at 4 heads of 64): 13 us, the bytes alone 4.8 us;
-// 16 heads of 64: 23 us, 16 heads of 128 (64 MB): 34 us; one row of 131,072 tokens, 4 heads of 64: 20 us (67 MB, 3.3 TB/s).
+// of the registers).  16 rows of 256 - 8,192 tokens (61,000 in all, 31 MB at 4 heads of 64): 12 us, the bytes alone 4.8 us;
+// 16 heads of 64: 23 us, 16 heads of 128 (64 MB): 34 us; lists of 32 pages, 16 rows, 4 heads of 64 (17 MB): 10 us; one row of 131,072 tokens, 4 heads of 64: 20 us (67 MB, 3.3 TB/s).
 // Two CTAs per SM with half the registers, and the next batch's keys loaded a batch ahead, were both slower.
 #include <algorithm>
 
@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(32 * NW) paged_simt_kernel(const PsArgs a) {
 // values each where Dv % 4 == 0, else single ones).  Bound by latency, so it is the number of warps in flight that counts.
 // Few rows have many parts each: with eight warps per head a 1M-token row (74 parts of 128 heads) takes 8 us, part after part
 // 90 us.  Many rows have few: the 32-row decode batch (3.3 parts each) takes 5 us with a warp per head, 28 us with sixteen.
+// The bf16 forms of several warps per head spill 28 bytes at four CTAs per SM.
 constexpr int kPcThreads = 256, kPcWarps = kPcThreads / 32;
 
 // kBlocks: workers / 32, rounded up.  Four CTAs per SM, so that the decode batch's 4,096 warps run in one wave.

@@ -24,10 +24,11 @@
 //              page's ninth block, half in one of two 4 KB buffers, so that two pages of it are in flight.
 // P is rounded to bf16 for P V, as the tensor cores take it (2^-8 of a weight); the sum l keeps the unrounded weights in fp32.
 //
-// Measured on one B200, the join included: 1 row of 1,048,576 tokens 261 - 275 us (4.5 TB/s of keys, 1.1 PFLOP/s) in short
-// bursts, 314 us in a loop of seconds, where the 1000 W cap holds the SM clock at 1.3 - 1.6 GHz; 32 rows of 4K - 32K tokens
-// 129 us, 155 us in a loop (DRAM 54 %, tensor pipe 53 % busy); 61 rows up to 8K, 16 heads, 68 us; 1 row of 130 tokens 11 us.
-// A page takes 1.2 us of a pair: 0.83 us is what DRAM gives, 1,425 cycles the matrix instructions (QK^T 36 steps of 25.3
+// Measured on one B200, whole calls (the join included) back to back for seconds, where the 1000 W cap holds the SM clock: 1 row
+// of 1,048,576 tokens 323 us at 1.33 GHz (3.7 TB/s of keys, 0.9 PFLOP/s; 278 us in bursts of four calls at full clock); 32 rows of
+// 4K - 32K tokens 158 us at 1.42 GHz (140 in bursts, of which this kernel 129: DRAM 54 %, tensor pipe 53 % busy); 61 rows up
+// to 8K, 16 heads, 81 us at 1.61 GHz; 1 row of 130 tokens 11 us.
+// A page takes 1.2 us of a pair at full clock: 0.83 us is what DRAM gives, 1,425 cycles the matrix instructions (QK^T 36 steps of 25.3
 // cycles, held by the operand reads at N = 64; P V 8 of 64.3), and what is left is the way of a buffer through copy, QK^T,
 // softmax, P V.
 // What lost: QK^T of two pages as one N = 128 instruction (32.3 cycles a step, but a page then waits for the next one: 1M row

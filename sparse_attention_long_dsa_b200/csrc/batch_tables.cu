@@ -13,8 +13,9 @@
 // A plan (one CTA: a scan over the sequences) decides everything before anything is written, so that a step that does
 // not fit changes neither the tables nor the stack; the expansion is one thread per four query rows.  The first row of
 // a page (pos % 64 == 0, always one of the step's rows when the page is new) also writes the table entry, so pages
-// need no pass of their own.  Bound by latency (a few bytes per sequence and 12 per row): 4.4 us for a decode step of 32
-// sequences, 6.3 us for two 8,192-row chunks beside 16 decodes, 8.6 us for 64 prompts of 1 to 16,384 rows (6.7 MB).
+// need no pass of their own.  Bound by latency (a few bytes per sequence and 12 per row).  On the device: 4.2 us for a decode
+// step of 32 sequences, 5.9 us for two 8,192-row chunks beside 16 decodes, 8.4 us for 64 prompts of 1 to 16,384 rows (6.7 MB).
+// Release, a CTA per sequence: 4.2 us for 32 sequences of 512 pages, 8.5 us for one of 16,384.
 #include <algorithm>
 
 #include "common.cuh"

@@ -81,7 +81,8 @@ class PagedCache:
         """The step's rows, total_q of them (a decode step: num_seqs): kv [total_q, 576] (512 normed by kv_weight, 64 rotated in
         pairs) and k_idx [total_q, 128] (normed by k_idx_weight, its first 64 rotated in halves, e4m3 with a scale) go to their
         slots; q_rot [total_q, heads, 64] is rotated into q[:, :, 512:] and q_idx [total_q, 64, 128] (first 64 rotated in halves)
-        into q_idx_out as e4m3 codes, row by row.  Up to three of them may be left out.  A packed step of num_seqs rows makes
+        into q_idx_out as e4m3 codes of the values themselves (no scale: +-448 at most), row by row; rows without a position stay as
+        they were.  Up to three of them may be left out.  A packed step of num_seqs rows makes
         a q that attend would take with its rows shifted behind a slot without a new token: it is refused unless packed says
         that the packed rows are meant."""
         for name, x, dest, what in (("q_rot", q_rot, q, "q"), ("q_idx", q_idx, q_idx_out, "q_idx_out")):
